@@ -54,11 +54,21 @@ typedef struct CUstream_st *int8mm_stream_t; /* the same type as cudaStream_t */
 #define INT8MM_ERR_TIMEOUT (-8)      /* device side: a bounded wait gave up */
 #define INT8MM_ERR_OVERFLOW (-9)     /* device side: an outlier count beyond K */
 #define INT8MM_ERR_SCRATCH (-10)     /* shape beyond int8_linear_forward_noalloc's scratch */
-#define INT8MM_ERR_FLAGS (-11)       /* unknown bits in the flags of int8_linear_forward_ex */
+#define INT8MM_ERR_FLAGS (-11)       /* unknown bits in the flags argument */
+#define INT8MM_ERR_GROUP (-12)       /* int4_*: the group size is not 32, 64 or a multiple of 128 */
+#define INT8MM_ERR_VALUE (-13)       /* eps negative or not finite, or a scale not finite */
 
 /* flags of int8_linear_forward_ex */
 #define INT8MM_PER_TENSOR_SCALE 1u   /* one activation scale for the whole of X */
 #define INT8MM_PAIR_TILES 2u         /* M > 128: 256 x 256 product tiles on CTA pairs */
+
+/* flags of the int4_* calls, int8_block_norm and int8_block_residual */
+#define INT8MM_BFLOAT16 1u           /* the call's 16-bit type T is bfloat16 (otherwise binary16) */
+/* flags of int8_block_norm and int8_block_residual */
+#define INT8MM_LAYER_NORM 2u         /* subtract the row's mean (otherwise root-mean-square norm) */
+#define INT8MM_F32_RESIDUAL 4u       /* the residual rows (x, y) are float32 (otherwise T) */
+/* flag of int8_block_residual */
+#define INT8MM_POST_NORM 8u          /* normalize the block's output before it is added */
 
 /* Bytes of the static device scratch behind int8_linear_forward_noalloc (per device). */
 #define INT8MM_NOALLOC_SCRATCH_BYTES (512 * 1024)
@@ -306,6 +316,108 @@ int int8_linear_forward_trace(const void *X, int M, int K, const int8_t *Wq,
 int int8_linear_forward_noalloc(const void *X, int M, int K, const int8_t *Wq,
                                 const float *w_scale, const void *bias, int N, float threshold,
                                 void *Y, int32_t *dev_status, int8mm_stream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit weights
+ *
+ * The linear layer whose weights are held in 4 bits with one scale (and, on request, one zero
+ * point) for every `group` consecutive input features of an output channel, for the layers
+ * whose weights' bytes are the cost: few tokens.  The activations stay in 16 bits.
+ *
+ * T is the 16-bit type of the call: binary16, or bfloat16 with INT8MM_BFLOAT16 in flags; X, W,
+ * scales, bias, Y and W_hat are all of type T.
+ *   codes   uint8 [N, K/2]           u[n,k] in 0..15, 8 to a 32-bit little-endian word: word j of
+ *                                    row n holds k = 8j .. 8j+7, its nibbles from the low end
+ *                                    k = 8j + 0, 2, 4, 6, 1, 3, 5, 7
+ *   scales  T     [N, ceil(K/group)]
+ *   zeros   uint8 [N, ceil(K/group)] whole numbers 0..15, or NULL: every zero point is 8
+ * and they stand for W_hat[n,k] = scales[n,c] * (u[n,k] - zeros[n,c]), c = k / group.
+ * group is 32, 64 or a multiple of 128 (else INT8MM_ERR_GROUP); it may exceed K, and the last
+ * group of a row may be short.  K must be a multiple of 32, 1 <= N, K <= INT8MM_MAX_K.  The
+ * conventions at the top of this file hold for these calls too.
+ */
+
+/*
+ * Quantize W once, when the layer is loaded; per group, with the maxima over its columns,
+ * rne = round to nearest, ties to even, quotients float32 IEEE:
+ *   zeros == NULL:  s = T(max |w| / 7);                  u = 8 + clamp(rne(w / s), -7, 7)
+ *   otherwise:      lo = min(w, 0), hi = max(w, 0);      s = T(hi / 15 - lo / 15);
+ *                   z = clamp(rne(-lo / s), 0, 15);      u = clamp(rne(w / s) + z, 0, 15)
+ * The codes are taken with the scale as it is stored.  A group whose scale is 0 (all zeros, or
+ * too small for T) gets codes equal to its zero point (8, or 0).  A group that holds a NaN or an
+ * infinity gets the scale NaN and codes equal to its zero point 8: every product with it is NaN.
+ *   W       [in]  T [N, K]
+ *   codes, scales, zeros [out] as above; zeros may be NULL
+ */
+int int4_quant_weight(const void *W, int N, int K, int group, unsigned flags, uint8_t *codes,
+                      void *scales, uint8_t *zeros, int8mm_stream_t stream);
+
+/*
+ * What the codes stand for: W_hat[n,k] = T(scales[n,c] * (u[n,k] - zeros[n,c])), rounded once.
+ *   W_hat [out] T [N, K]
+ */
+int int4_dequant_weight(const uint8_t *codes, const void *scales, const uint8_t *zeros, int N,
+                        int K, int group, unsigned flags, void *W_hat, int8mm_stream_t stream);
+
+/*
+ * The linear layer on 4-bit weights:
+ *   Y[m,n] = T( sum_k X[m,k] * W_hat[n,k] + bias[n] )            (float32 sums)
+ *   X          [in]  T [M, K], M >= 1
+ *   codes, scales, zeros [in] as above (zeros may be NULL)
+ *   bias       [in]  T [N], or NULL for none
+ *   Y          [out] T [M, N]; must not overlap an input
+ *   dev_status [in/out] one int32 of device memory that receives a negative code if a bounded
+ *              device-side wait gives up (zero it first), or NULL to not be told
+ * No workspace: calls on different streams do not disturb each other.
+ */
+int int4_linear_forward(const void *X, int M, int K, const uint8_t *codes, const void *scales,
+                        const uint8_t *zeros, const void *bias, int N, int group, unsigned flags,
+                        void *Y, int32_t *dev_status, int8mm_stream_t stream);
+
+/* ------------------------------------------------------------------ norms around a block
+ *
+ * The row passes before and after a block of linear layers (attention or feed-forward): the norm
+ * that makes its input, and the gate, the residual sum and the norms after it.  Rows have D
+ * elements, D a multiple of 16, 1 <= D <= INT8MM_MAX_K; M >= 1 rows.
+ *
+ * T is the 16-bit type as above; R, the type of the residual rows, is T, or float32 with
+ * INT8MM_F32_RESIDUAL.  norm(v; w, b)[j] = n(v)[j] * w[j] + b[j] with
+ *   n(v) = v / sqrt(mean(v^2) + eps), or, with INT8MM_LAYER_NORM,
+ *   n(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps),
+ * w NULL = all ones, b NULL = all zeros; statistics and products in float32, rounded once where
+ * a result is stored.  eps >= 0 and finite (else INT8MM_ERR_VALUE).
+ */
+
+/*
+ * Before a block: h = T(norm(x; weight, bias)).
+ *   x            [in]  R [M, D]
+ *   weight, bias [in]  T [D], or NULL
+ *   h            [out] T [M, D]; may be x itself when R is T
+ */
+int int8_block_norm(const void *x, int M, int D, const void *weight, const void *bias, float eps,
+                    unsigned flags, void *h, int8mm_stream_t stream);
+
+/*
+ * After a block, and before the next one:
+ *   p = norm(f; post_weight, post_bias)  with INT8MM_POST_NORM, otherwise p = f
+ *   y = R(x_scale * x + f_scale * gate * p)
+ *   h = T(norm(y; next_weight, next_bias))           (of y as it is stored)
+ *   f            [in]  T [M, D], the block's output
+ *   x            [in]  R [M, D], the residual rows
+ *   post_weight, post_bias [in] T [D], or NULL (must be NULL without INT8MM_POST_NORM)
+ *   gate         [in]  T [gate_rows, D], or NULL with gate_rows = 0: row m of f is multiplied by
+ *                      row m / (M / gate_rows) (1 row: a gate for every channel; one per
+ *                      sequence of a batch; M rows: one per token).  M % gate_rows == 0.
+ *   x_scale, f_scale [in] finite numbers
+ *   next_weight, next_bias [in] T [D], or NULL (must be NULL when h is NULL)
+ *   y            [out] R [M, D], or NULL if only h is wanted; may be x itself
+ *   h            [out] T [M, D], or NULL for no norm of the sum; may be f itself
+ * At least one of y and h is given.  Apart from the two cases named, outputs do not overlap
+ * inputs or each other.
+ */
+int int8_block_residual(const void *f, const void *x, int M, int D, const void *post_weight,
+                        const void *post_bias, const void *gate, int gate_rows, float x_scale,
+                        float f_scale, const void *next_weight, const void *next_bias, float eps,
+                        unsigned flags, void *y, void *h, int8mm_stream_t stream);
 
 /*
  * Waits for `stream`, then returns the device status word at dev_status (for the forward

@@ -8,9 +8,13 @@ built, importing the binding's functions raises.
 Functions keep the C names:
     int8_quant_weight, int8_linear_workspace_size, int8_linear_forward,
     int8_quantize_rows, int8_gemm_i32, int8_outlier_weights, int8_read_device_status,
-    int8_status_string, int8_linear_forward_noalloc
+    int8_status_string, int8_linear_forward_noalloc,
+    int4_quant_weight, int4_dequant_weight, int4_linear_forward,
+    int8_block_norm, int8_block_residual
 and ``Int8Linear`` bundles them the way the pages use the layer
-(``Linear8bitLt(in, out, bias, has_fp16_weights=False, threshold=6.0)``).
+(``Linear8bitLt(in, out, bias, has_fp16_weights=False, threshold=6.0)``); ``Int4Linear`` is the
+layer on 4-bit weights with group scales, and ``BlockNorm`` the norms either layer can be given
+for the row passes before and after its block.
 """
 from __future__ import annotations
 
@@ -30,11 +34,16 @@ __all__ = [
     "int8_linear_forward_fp16w", "int8_linear_forward_ex", "PER_TENSOR_SCALE",
     "int8_activation_stats", "Int8Linear", "DEFAULT_THRESHOLD", "int8_linear_forward_trace",
     "int8_outlier_row", "PAIR_TILES",
+    "int4_quant_weight", "int4_dequant_weight", "int4_linear_forward", "Int4Linear",
+    "int8_block_norm", "int8_block_residual", "BlockNorm",
 ]
 
 DEFAULT_THRESHOLD = 6.0
 PER_TENSOR_SCALE = 1  # int8_linear_forward_ex flag: one activation scale for the whole of X
 PAIR_TILES = 2        # int8_linear_forward_ex flag: M > 128 products on CTA pairs (256 x 256)
+# flags of the int4_* calls and the block norms
+_BFLOAT16, _LAYER_NORM, _F32_RESIDUAL, _POST_NORM = 1, 2, 4, 8
+_HALF_TYPES = (torch.float16, torch.bfloat16)
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libint8mm.so")
 _lib = None
@@ -85,7 +94,15 @@ def load_library():
         lib.int8_activation_stats_workspace_size.restype = sz
         lib.int8_activation_stats.argtypes = [p, i, i, p, p, p, sz, p]
         lib.int8_outlier_row.argtypes = [p, i, f, p, p]
-        for name in ("int8_quant_weight", "int8_linear_forward", "int8_linear_quantize",
+        u = ctypes.c_uint
+        lib.int4_quant_weight.argtypes = [p, i, i, i, u, p, p, p, p]
+        lib.int4_dequant_weight.argtypes = [p, p, p, i, i, i, u, p, p]
+        lib.int4_linear_forward.argtypes = [p, i, i, p, p, p, p, i, i, u, p, p, p]
+        lib.int8_block_norm.argtypes = [p, i, i, p, p, f, u, p, p]
+        lib.int8_block_residual.argtypes = [p, p, i, i, p, p, p, i, f, f, p, p, f, u, p, p, p]
+        for name in ("int4_quant_weight", "int4_dequant_weight", "int4_linear_forward",
+                     "int8_block_norm", "int8_block_residual",
+                     "int8_quant_weight", "int8_linear_forward", "int8_linear_quantize",
                      "int8_linear_matmul", "int8_linear_forward_acc", "int8_quantize_rows",
                      "int8_gemm_i32", "int8_outlier_weights", "int8_read_device_status",
                      "int8_linear_forward_noalloc", "int8_linear_forward_fp16w",
@@ -453,7 +470,271 @@ def int8_read_device_status(dev_status: torch.Tensor, stream=None) -> int:
         _ptr(dev_status), ctypes.c_void_p(_stream(stream, dev_status.device))))
 
 
-class Int8Linear:
+# ------------------------------------------------------------------ 4-bit weights, block norms
+
+def _tensor(t: torch.Tensor, dtype, shape: tuple, like: torch.Tensor, name: str) -> int:
+    """The address of a contiguous CUDA tensor of this dtype and shape on `like`'s device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {like.device}")
+    return t.data_ptr()
+
+
+def _half(t: torch.Tensor, name: str) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _HALF_TYPES:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output tensor whose memory belongs to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _call(fn, what: str, like: torch.Tensor, stream, *args) -> None:
+    """fn(*args, stream) with like's device current; raises on a nonzero status."""
+    index = like.get_device()
+    if index == torch.cuda.current_device():
+        status = fn(*args, _stream(stream, index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(stream, index))
+    if status != 0:
+        raise Int8mmError(status, what)
+
+
+def _int4_shapes(K: int, group_size: int) -> int:
+    """Groups of a row (1 for a group size the library is left to refuse)."""
+    return -(-K // group_size) if group_size > 0 else 1
+
+
+def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = True,
+                      codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                      zeros: torch.Tensor | None = None, stream=None):
+    """(codes, scales, zeros) of an fp16 or bf16 [N, K] weight: 4-bit codes packed in uint8
+    [N, K/2] (their order is in int8mm.h), one scale of W's type for every group_size input
+    features, and, unless symmetric, one zero point (uint8) for each; zeros is None if
+    symmetric."""
+    _half(W, "W")
+    N, K = W.shape
+    groups = _int4_shapes(K, group_size)
+    if symmetric and zeros is not None:
+        raise ValueError("zeros is an output of the asymmetric quantizer: pass symmetric=False")
+    if codes is None:
+        codes = _new((N, K // 2), torch.uint8, W, stream)
+    if scales is None:
+        scales = _new((N, groups), W.dtype, W, stream)
+    if zeros is None and not symmetric:
+        zeros = _new((N, groups), torch.uint8, W, stream)
+    _call(load_library().int4_quant_weight, "int4_quant_weight", W, stream,
+          W.data_ptr(), N, K, group_size, W.dtype is torch.bfloat16,
+          _tensor(codes, torch.uint8, (N, K // 2), W, "codes"),
+          _tensor(scales, W.dtype, (N, groups), W, "scales"),
+          None if symmetric else _tensor(zeros, torch.uint8, (N, groups), W, "zeros"))
+    return codes, scales, zeros
+
+
+def _int4_operands(codes, scales, zeros, group_size: int):
+    """(N, K, addresses) of a 4-bit weight, checked against each other."""
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        raise TypeError("codes must be a CUDA tensor")
+    if scales.dtype not in _HALF_TYPES:
+        raise TypeError(f"scales must be torch.float16 or torch.bfloat16, got {scales.dtype}")
+    if codes.dim() != 2:
+        raise ValueError("codes must have 2 dimensions")
+    N, K = codes.shape[0], codes.shape[1] * 2
+    shape = (N, _int4_shapes(K, group_size))
+    return (N, K, _tensor(codes, torch.uint8, codes.shape, codes, "codes"),
+            _tensor(scales, scales.dtype, shape, codes, "scales"),
+            None if zeros is None else _tensor(zeros, torch.uint8, shape, codes, "zeros"))
+
+
+def int4_dequant_weight(codes: torch.Tensor, scales: torch.Tensor,
+                        zeros: torch.Tensor | None = None, group_size: int = 128,
+                        W_hat: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """What the codes stand for: scales * (code - zero) of scales' type, [N, K]."""
+    N, K, c, s, z = _int4_operands(codes, scales, zeros, group_size)
+    if W_hat is None:
+        W_hat = _new((N, K), scales.dtype, codes, stream)
+    _call(load_library().int4_dequant_weight, "int4_dequant_weight", codes, stream, c, s, z, N, K,
+          group_size, scales.dtype is torch.bfloat16,
+          _tensor(W_hat, scales.dtype, (N, K), codes, "W_hat"))
+    return W_hat
+
+
+def int4_linear_forward(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                        zeros: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                        group_size: int = 128, Y: torch.Tensor | None = None,
+                        dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X . W_hat^T + bias, [M, N] of X's type (fp16 or bf16), on the 4-bit weights of
+    int4_quant_weight.  dev_status: an int32 that receives a device-side failure code."""
+    _half(X, "X")
+    N, K, c, s, z = _int4_operands(codes, scales, zeros, group_size)
+    T = X.dtype
+    M = X.shape[0]
+    if scales.dtype is not T:
+        raise TypeError(f"scales must be {T} like X, got {scales.dtype}")
+    if X.shape[1] != K:
+        raise ValueError(f"X must have {K} columns, got {X.shape[1]}")
+    if Y is None:
+        Y = _new((M, N), T, X, stream)
+    _call(load_library().int4_linear_forward, "int4_linear_forward", X, stream,
+          _tensor(X, T, X.shape, codes, "X"), M, K, c, s, z,
+          None if bias is None else _tensor(bias, T, (N,), codes, "bias"), N, group_size,
+          T is torch.bfloat16, _tensor(Y, T, (M, N), codes, "Y"),
+          None if dev_status is None
+          else _tensor(dev_status, torch.int32, (1,), codes, "dev_status"))
+    return Y
+
+
+def _rows(x: torch.Tensor, name: str) -> None:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if x.dtype not in _HALF_TYPES and x.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def int8_block_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+                    bias: torch.Tensor | None = None, eps: float = 1e-6,
+                    layer_norm: bool = False, h: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """h = norm(x) * weight + bias for the rows of x [M, D]: the root-mean-square norm, or the
+    layer norm (layer_norm=True).  x is fp16, bf16, or float32 (a residual stream kept in 32
+    bits; h then has the type of weight, or of the h given, or fp16).  h may be x itself."""
+    _rows(x, "x")
+    M, D = x.shape
+    if x.dtype is not torch.float32:
+        T = x.dtype
+    elif weight is not None:
+        T = weight.dtype
+    else:
+        T = torch.float16 if h is None else h.dtype
+    if T not in _HALF_TYPES:
+        raise TypeError(f"weight and h must be torch.float16 or torch.bfloat16, got {T}")
+    if h is None:
+        h = _new((M, D), T, x, stream)
+    flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
+             | (_F32_RESIDUAL if x.dtype is torch.float32 else 0))
+    _call(load_library().int8_block_norm, "int8_block_norm", x, stream, x.data_ptr(), M, D,
+          None if weight is None else _tensor(weight, T, (D,), x, "weight"),
+          None if bias is None else _tensor(bias, T, (D,), x, "bias"), eps, flags,
+          _tensor(h, T, (M, D), x, "h"))
+    return h
+
+
+def int8_block_residual(f: torch.Tensor, x: torch.Tensor, post_norm: bool = False,
+                        post_weight: torch.Tensor | None = None,
+                        post_bias: torch.Tensor | None = None,
+                        gate: torch.Tensor | None = None, x_scale: float = 1.0,
+                        f_scale: float = 1.0, next_norm: bool = False,
+                        next_weight: torch.Tensor | None = None,
+                        next_bias: torch.Tensor | None = None, eps: float = 1e-6,
+                        layer_norm: bool = False, y: torch.Tensor | None = None,
+                        h: torch.Tensor | None = None, stream=None):
+    """(y, h) after a block with output f [M, D] on the residual rows x [M, D]:
+    y = x_scale * x + f_scale * gate * norm(f) (no norm unless post_norm) and, with next_norm,
+    h = norm(y), the next block's input (otherwise h is None), in one pass.
+
+    f is fp16 or bf16; x has f's type or is float32, and y has x's.  gate is [Gr, D] or [D]: row
+    m of f takes gate row m // (M / Gr).  y may be x itself, h may be f itself."""
+    _half(f, "f")
+    _rows(x, "x")
+    T, R = f.dtype, x.dtype
+    M, D = f.shape
+    if R is not T and R is not torch.float32:
+        raise TypeError(f"x must be {T} like f, or float32, got {R}")
+    if not post_norm and (post_weight is not None or post_bias is not None):
+        raise ValueError("post_weight and post_bias need post_norm=True")
+    if not next_norm and (next_weight is not None or next_bias is not None or h is not None):
+        raise ValueError("next_weight, next_bias and h need next_norm=True")
+    gate_rows = 0
+    if gate is not None:
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+        if gate_rows <= 0 or M % gate_rows:
+            raise ValueError(f"gate has {gate_rows} rows, which do not divide the {M} rows of f")
+    if y is None:
+        y = _new((M, D), R, f, stream)
+    if h is None and next_norm:
+        h = _new((M, D), T, f, stream)
+    flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
+             | (_F32_RESIDUAL if R is not T else 0) | (_POST_NORM if post_norm else 0))
+    _call(load_library().int8_block_residual, "int8_block_residual", f, stream, f.data_ptr(),
+          _tensor(x, R, (M, D), f, "x"), M, D,
+          None if post_weight is None else _tensor(post_weight, T, (D,), f, "post_weight"),
+          None if post_bias is None else _tensor(post_bias, T, (D,), f, "post_bias"),
+          None if gate is None
+          else _tensor(gate, T, (gate_rows, D) if gate.dim() == 2 else (D,), f, "gate"),
+          gate_rows, x_scale, f_scale,
+          None if next_weight is None else _tensor(next_weight, T, (D,), f, "next_weight"),
+          None if next_bias is None else _tensor(next_bias, T, (D,), f, "next_bias"), eps, flags,
+          _tensor(y, R, (M, D), f, "y"), None if h is None else _tensor(h, T, (M, D), f, "h"))
+    return y, h
+
+
+class BlockNorm:
+    """A norm with its weights, as the layers take it (``pre_norm``, ``post_norm``): the
+    root-mean-square norm, or the layer norm with ``layer_norm=True``."""
+
+    def __init__(self, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-6, layer_norm: bool = False):
+        self.weight, self.bias = weight, bias
+        self.eps, self.layer_norm = float(eps), bool(layer_norm)
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        h = int8_block_norm(x2, self.weight, self.bias, self.eps, self.layer_norm, h=out)
+        return h.reshape(x.shape)
+
+
+class _BlockEnds:
+    """What the layers share around their product: the norm of the input, and the gate and the
+    residual sum of the output."""
+
+    pre_norm: BlockNorm | None = None
+    post_norm: BlockNorm | None = None
+
+    def _before(self, X: torch.Tensor) -> torch.Tensor:
+        X2 = X.reshape(-1, X.shape[-1]).contiguous()
+        return X2 if self.pre_norm is None else self.pre_norm(X2)
+
+    def _after(self, Y: torch.Tensor, residual, gate, x_scale, f_scale, out):
+        post = self.post_norm
+        r = residual.reshape(Y.shape).contiguous()
+        return int8_block_residual(
+            Y, r, post_norm=post is not None, post_weight=post and post.weight,
+            post_bias=post and post.bias, gate=gate, x_scale=x_scale, f_scale=f_scale,
+            eps=post.eps if post is not None else 1e-6,
+            layer_norm=post is not None and post.layer_norm, y=out)[0]
+
+    def _finish(self, product, X, residual, gate, x_scale, f_scale, out):
+        """product(X2, out) between the block's ends."""
+        if residual is None and (gate is not None or self.post_norm is not None
+                                 or x_scale != 1.0 or f_scale != 1.0):
+            raise ValueError("gate, x_scale, f_scale and post_norm act where the layer's output "
+                             "is added to a residual")
+        if residual is None:
+            return product(self._before(X), out)
+        return self._after(product(self._before(X), None), residual, gate, x_scale, f_scale, out)
+
+
+class Int8Linear(_BlockEnds):
     """An LLM.int8() linear layer.
 
     Mirrors ``Linear8bitLt(in_features, out_features, bias, has_fp16_weights, threshold)``:
@@ -464,13 +745,19 @@ class Int8Linear:
     layer also keeps the fp16 weight and the outlier columns use it.  With
     ``per_tensor_activation=True`` one activation scale serves the whole input (the default is
     one per row).
+
+    The layer at the start of a block can be given the block's ``pre_norm``; the layer at its end
+    is called with the ``residual`` rows its output is added to: the result is then
+    x_scale * residual + f_scale * gate * post_norm(output) (int8_block_residual).
     """
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None,
                  threshold: float = DEFAULT_THRESHOLD, has_fp16_weights: bool = False,
-                 per_tensor_activation: bool = False):
+                 per_tensor_activation: bool = False, pre_norm: BlockNorm | None = None,
+                 post_norm: BlockNorm | None = None):
         if math.isnan(threshold):
             raise ValueError("threshold is NaN")
+        self.pre_norm, self.post_norm = pre_norm, post_norm
         self.out_features, self.in_features = weight.shape
         weight = weight.to(torch.float16).contiguous()
         self.Wq, self.w_scale = int8_quant_weight(weight)
@@ -487,17 +774,59 @@ class Int8Linear:
             self._ws_rows = M
         return self._workspace
 
-    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None,
+                 residual: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                 x_scale: float = 1.0, f_scale: float = 1.0) -> torch.Tensor:
         lead = X.shape[:-1]
-        X2 = X.reshape(-1, self.in_features).contiguous()
+        Y = self._finish(self._product, X, residual, gate, x_scale, f_scale, out)
+        return Y.reshape(*lead, self.out_features)
+
+    def _product(self, X2: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
+        X2 = X2.reshape(-1, self.in_features)
         ws = self._ws(X2.shape[0], X2.device)
         if self.per_tensor_activation:
-            Y = int8_linear_forward_ex(X2, self.Wq, self.w_scale, self.bias, self.threshold,
-                                       W16=self.W16, per_tensor=True, Y=out, workspace=ws)
-        elif self.W16 is not None:
-            Y = int8_linear_forward_fp16w(X2, self.Wq, self.w_scale, self.W16, self.bias,
-                                          self.threshold, Y=out, workspace=ws)
-        else:
-            Y = int8_linear_forward(X2, self.Wq, self.w_scale, self.bias, self.threshold, Y=out,
-                                    workspace=ws)
+            return int8_linear_forward_ex(X2, self.Wq, self.w_scale, self.bias, self.threshold,
+                                          W16=self.W16, per_tensor=True, Y=out, workspace=ws)
+        if self.W16 is not None:
+            return int8_linear_forward_fp16w(X2, self.Wq, self.w_scale, self.W16, self.bias,
+                                             self.threshold, Y=out, workspace=ws)
+        return int8_linear_forward(X2, self.Wq, self.w_scale, self.bias, self.threshold, Y=out,
+                                   workspace=ws)
+
+
+class Int4Linear(_BlockEnds):
+    """A linear layer on 4-bit weights with group scales.
+
+    The fp16 or bf16 weight [out, in] is quantized once at construction, each ``group_size``
+    input features of an output channel with a scale (and, with ``symmetric=False``, a zero
+    point) of their own; ``in_features`` is a multiple of 32.  Calls take activations of the
+    weight's type, from one token to a long prompt.  ``pre_norm``, ``post_norm`` and the call's
+    ``residual`` are as for ``Int8Linear``.
+    """
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                 group_size: int = 128, symmetric: bool = True,
+                 pre_norm: BlockNorm | None = None, post_norm: BlockNorm | None = None):
+        self.out_features, self.in_features = weight.shape
+        self.group_size = int(group_size)
+        self.pre_norm, self.post_norm = pre_norm, post_norm
+        weight = weight.contiguous()
+        self.codes, self.scales, self.zeros = int4_quant_weight(weight, self.group_size,
+                                                                symmetric)
+        self.bias = None if bias is None else bias.to(weight.dtype).contiguous()
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=weight.device)
+
+    def dequantize(self) -> torch.Tensor:
+        """The weight the codes stand for, [out, in]."""
+        return int4_dequant_weight(self.codes, self.scales, self.zeros, self.group_size)
+
+    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None,
+                 residual: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                 x_scale: float = 1.0, f_scale: float = 1.0) -> torch.Tensor:
+        lead = X.shape[:-1]
+        Y = self._finish(self._product, X, residual, gate, x_scale, f_scale, out)
         return Y.reshape(*lead, self.out_features)
+
+    def _product(self, X2: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
+        return int4_linear_forward(X2, self.codes, self.scales, self.zeros, self.bias,
+                                   self.group_size, Y=out, dev_status=self.dev_status)

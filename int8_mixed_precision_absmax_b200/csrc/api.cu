@@ -82,6 +82,8 @@ const char* int8_status_string(int status) {
     case INT8MM_ERR_SCRATCH:
       return "the shape needs more scratch than the library's static buffer holds";
     case INT8MM_ERR_FLAGS: return "unknown flag bits";
+    case INT8MM_ERR_GROUP: return "the group size is not 32, 64 or a multiple of 128";
+    case INT8MM_ERR_VALUE: return "eps is negative or not finite, or a scale is not finite";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,117 @@
+// block.cuh -- internal interface of the 4-bit weights (int4.cu) and the block norms (norm.cu):
+// what their entry points (api_block.cu) hand to the kernels' launches.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "int8mm.h"
+
+namespace i8mm {
+
+// ---------------------------------------------------------------- 16-bit types
+
+template <typename T>
+struct Half2Of;
+template <>
+struct Half2Of<__half> {
+  using type = __half2;
+};
+template <>
+struct Half2Of<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
+
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+
+// Two neighbours in one 32-bit word, low half first.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+//
+// Of the 8 neighbours k = 8j .. 8j+7 in a 32-bit word, nibble i (from the low end) holds
+// k = 8j + kInt4Order(i): 0, 2, 4, 6, 1, 3, 5, 7.  One AND with 0x000F000F (of the word shifted
+// right by 0, 4, 8, 12) leaves the neighbours (0,1), (2,3), (4,5), (6,7) in the two halves of a
+// register, the order in which a 16-byte load of X holds their factors.
+__host__ __device__ constexpr int int4_order(int i) { return i < 4 ? 2 * i : 2 * i - 7; }
+// The nibble that holds neighbour j of its word.
+__host__ __device__ constexpr int int4_nibble(int j) { return (j & 1) * 4 + (j >> 1); }
+
+constexpr int kInt4Zero = 8;  // the zero point where none is given
+
+struct Int4Weight {
+  const uint8_t* codes;
+  const void* scales;    // T [N, groups]
+  const uint8_t* zeros;  // [N, groups] or null
+  int N, K, group, groups;
+  bool bf16;
+};
+inline int int4_groups(int K, int group) { return (K + group - 1) / group; }
+
+struct Int4LinearArgs {
+  Int4Weight w;
+  const void* X;     // T [M, K]
+  const void* bias;  // T [N] or null
+  void* Y;           // T [M, N]
+  int M;
+  int32_t* status;   // nullable
+};
+
+cudaError_t launch_int4_quant(const void* W, int N, int K, int group, bool bf16, uint8_t* codes,
+                              void* scales, uint8_t* zeros, int num_sms, cudaStream_t stream);
+cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
+                                cudaStream_t stream);
+cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- block norms
+
+struct BlockNormArgs {
+  const void* f;            // T [M, D], or null: the norm before a block alone
+  const void* x;            // R [M, D]
+  const void *post_w, *post_b, *gate, *next_w, *next_b;  // nullable
+  void* y;                  // R [M, D] or null
+  void* h;                  // T [M, D] or null
+  int M, D;
+  int gate_rows;            // 0 without a gate
+  float x_scale, f_scale, eps;
+  bool bf16, layer_norm, f32_residual, post_norm;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, int num_sms, cudaStream_t stream);
+
+}  // namespace i8mm
