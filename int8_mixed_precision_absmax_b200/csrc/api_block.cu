@@ -107,8 +107,9 @@ int int4_linear_forward(const void* X, int M, int K, const uint8_t* codes, const
   a.Y = Y;
   a.M = M;
   a.status = dev_status;
-  return launched(
-      launch_int4_linear(a, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return launched(M > 8 ? launch_int4_tile(a, device_sm_count(), st)
+                        : launch_int4_linear(a, device_sm_count(), st));
 }
 
 int int8_block_norm(const void* x, int M, int D, const void* weight, const void* bias, float eps,

@@ -98,6 +98,8 @@ cudaError_t launch_int4_quant(const void* W, int N, int K, int group, bool bf16,
 cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
                                 cudaStream_t stream);
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
+// the same product on the tensor cores (int4_tile.cu), for more than a few tokens
+cudaError_t launch_int4_tile(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- block norms
 

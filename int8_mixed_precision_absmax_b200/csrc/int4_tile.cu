@@ -1,0 +1,545 @@
+// int4_tile.cu -- the product on 4-bit weights for more than a few tokens, on the tensor cores.
+//
+//   D[n, m] = sum_k W_hat[n,k] X[m,k],   Y[m,n] = T(D[n,m] + bias[n])
+//
+// One tile is 128 output channels (the MMA's rows) by `tn` tokens (its columns).  The weights never
+// exist in 16 bits outside the SM: the dequantizing warps read the packed codes that TMA put into
+// shared memory, make W_hat = T(s (u - z)) in registers (u - z is exact, so one rounding to T: the
+// tensor core's operand type) and store it to tensor memory, from where tcgen05.mma takes its A
+// operand; X comes through TMA as the B operand.  Sums are float32 in tensor memory.
+//
+// Roles (448 threads): warps 0-7 dequantize (two for each quadrant of 32 tensor-memory lanes, each
+// 64 of a step's 128 k), warps 8-11 are the epilogue, warp 12 issues TMA, warp 13 allocates tensor
+// memory and issues the MMAs.  Rings: `stages` steps of codes and X in shared memory, `a_stages`
+// steps of W_hat and `d_slots` accumulators in tensor memory (two where they fit: the epilogue of
+// a tile overlaps the next tile's main loop).
+//
+// Few tiles: the K axis is split over the CTAs of a cluster, which leave their partial sums in
+// shared memory; each CTA then adds up a slice of the tokens from all of them, in rank order.
+//
+// Every wait is bounded (ptx.cuh); a wait that gives up reports INT8MM_ERR_TIMEOUT, and the block
+// drains its copies and MMAs, frees its tensor memory and exits.
+#include <type_traits>
+
+#include "block.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace i8mm {
+
+namespace {
+
+constexpr int kTileN = 128;   // channels per tile
+constexpr int kStepK = 128;   // k per step
+constexpr int kCodeBytes = kTileN * kStepK / 2;
+constexpr int kDequantWarps = 8, kEpiWarps = 4;
+constexpr int kTmaWarp = kDequantWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kMaxStages = 10, kMaxA = 4;
+constexpr int kACols = kStepK / 2;  // tensor-memory columns of a step of W_hat
+
+struct TileArgs {
+  const void* scales;
+  const uint8_t* zeros;
+  const void* bias;
+  void* Y;
+  int32_t* status;
+  int M, N, K, group, groups;
+  int tn, stages, a_stages, d_slots, tmem_cols, splits;
+  int m_tiles, tiles, steps;
+};
+
+struct TileShared {  // behind the ring
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t a_full[kMaxA], a_empty[kMaxA];
+  uint64_t d_full[2], d_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// tensor-memory columns from one accumulator to the next
+__host__ __device__ constexpr int slot_cols(int tn) { return (tn + 31) / 32 * 32; }
+__host__ __device__ constexpr int stage_bytes(int tn) { return kCodeBytes + tn * kStepK * 2; }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, float32 sums.  Issued by one thread.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void report(int32_t* status) {
+  if (status) atomicCAS(reinterpret_cast<int*>(status), 0, INT8MM_ERR_TIMEOUT);
+}
+
+// Every lane waits; the warp goes on together or gives up together (the tensor-memory accesses
+// that follow are warp-wide).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(~0u, mbar_wait_bounded(bar, parity, abort));
+}
+
+// 8 consecutive groups' scales and zero points of a row, from group g0 (a multiple of 8) on.  Groups
+// past the row's end repeat the last one (they meet zero activations only).
+struct GroupChunk {
+  uint32_t s[4], z[2];
+};
+template <typename T>
+__device__ __forceinline__ void load_chunk(GroupChunk& c, const T* scales, const uint8_t* zeros,
+                                           int g0, int groups) {
+  const uint16_t* s16 = reinterpret_cast<const uint16_t*>(scales);
+  if (g0 >= groups) return;  // a prefetch past the end
+  if ((groups & 7) == 0) {
+    const uint4 v = *reinterpret_cast<const uint4*>(s16 + g0);
+    c.s[0] = v.x, c.s[1] = v.y, c.s[2] = v.z, c.s[3] = v.w;
+    if (zeros) {
+      const uint2 w = *reinterpret_cast<const uint2*>(zeros + g0);
+      c.z[0] = w.x, c.z[1] = w.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = g0 + 2 * i;
+    if ((groups & 1) == 0 && g < groups) {
+      c.s[i] = *reinterpret_cast<const uint32_t*>(s16 + g);
+    } else {
+      c.s[i] = s16[min(g, groups - 1)] | static_cast<uint32_t>(s16[min(g + 1, groups - 1)]) << 16;
+    }
+  }
+  if (zeros) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c.z[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c.z[i] |= static_cast<uint32_t>(zeros[min(g0 + 4 * i + e, groups - 1)]) << (8 * e);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t chunk_scale2(const GroupChunk& c, int j) {  // in both halves
+  const uint32_t a = (j & 4) ? ((j & 2) ? c.s[3] : c.s[2]) : ((j & 2) ? c.s[1] : c.s[0]);
+  return __byte_perm(a, a, (j & 1) ? 0x3232 : 0x1010);
+}
+__device__ __forceinline__ uint32_t chunk_zero(const GroupChunk& c, int j) {
+  return (((j & 4) ? c.z[1] : c.z[0]) >> (8 * (j & 3))) & 0xFFu;
+}
+
+// W_hat of 4-bit words: the group's constants, and 8 values of a word.  A nibble set into the low
+// mantissa bits of 1024 (fp16) or 128 (bf16) reads as that number plus the code.
+template <typename T>
+struct Dequant;
+template <>
+struct Dequant<__half> {
+  __half2 s, z0, z1;
+  __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
+    s = *reinterpret_cast<const __half2*>(&s2);
+    const float zf = static_cast<float>(z);
+    z0 = __float2half2_rn(1024.0f + zf);   // exact up to 2048
+    z1 = __float2half2_rn(-64.0f - zf);    // of a code in bits 4..7: (1024 + 16 u) / 16
+  }
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    const uint32_t w8 = w >> 8;
+    const uint32_t a[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u,
+                           (w8 & 0x000F000Fu) | 0x64006400u, (w8 & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&a[i]);
+      const __half2 d = (i & 1) ? __hfma2(h, sixteenth, z1) : __hsub2(h, z0);
+      const __half2 v = __hmul2(d, s);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+template <>
+struct Dequant<__nv_bfloat16> {
+  __nv_bfloat162 s, z0;
+  __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
+    s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+    z0 = __float2bfloat162_rn(128.0f + static_cast<float>(z));
+  }
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      const __nv_bfloat162 v =
+          __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), z0), s);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+
+template <typename T>
+__host__ __device__ constexpr uint32_t tile_idesc(int n) {
+  return idesc_f16_f32(kTileN, n) | (sizeof(T) && std::is_same<T, __nv_bfloat16>::value
+                                         ? (1u << 7) | (1u << 10)
+                                         : 0u);
+}
+
+}  // namespace
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+    int4_tile_kernel(const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_w, const TileArgs p) {
+  extern __shared__ uint8_t tile_smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(tile_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int sbytes = stage_bytes(p.tn);
+  TileShared& S = *reinterpret_cast<TileShared*>(ring + p.stages * sbytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int s = 0; s < p.a_stages; ++s) {
+      mbar_init(&S.a_full[s], kDequantWarps);
+      mbar_init(&S.a_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&S.d_full[s], 1);
+      mbar_init(&S.d_empty[s], kEpiWarps);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_tmap(&map_x);
+    prefetch_tmap(&map_w);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&S.tmem_base, static_cast<uint32_t>(p.tmem_cols));
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  const uint32_t tmem = S.tmem_base;
+  const uint32_t a_base = tmem + static_cast<uint32_t>(p.d_slots * slot_cols(p.tn));
+  volatile int* abort = &S.abort;
+  // tiles t0, t0 + dt, ...; this CTA's part of the steps of each
+  const int split = p.splits > 1 ? static_cast<int>(blockIdx.x) % p.splits : 0;
+  const int t0 = static_cast<int>(blockIdx.x) / p.splits, dt = static_cast<int>(gridDim.x) / p.splits;
+  const int k_begin = static_cast<int>(static_cast<long long>(p.steps) * split / p.splits);
+  const int k_end = static_cast<int>(static_cast<long long>(p.steps) * (split + 1) / p.splits);
+  bool ok = true;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      for (int t = t0; ok && t < p.tiles; t += dt) {
+        const int m0 = t % p.m_tiles * p.tn, n0 = t / p.m_tiles * kTileN;
+        for (int k = k_begin; k < k_end; ++k) {
+          if (!mbar_wait_bounded(&S.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+          uint8_t* dst = ring + stage * sbytes;
+          mbar_arrive_expect_tx(&S.full[stage], static_cast<uint32_t>(sbytes));
+          tma_load_2d(&map_w, dst, &S.full[stage], k * (kStepK / 2), n0);
+          tma_load_2d(&map_x, dst + kCodeBytes, &S.full[stage], k * kStepK, m0);
+          tma_load_2d(&map_x, dst + kCodeBytes + p.tn * 128, &S.full[stage], k * kStepK + 64, m0);
+          ++issued;
+          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      int dummy = 0;  // every copy lands before the block can exit
+      for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; ++j)
+        mbar_wait_bounded(&S.full[j % p.stages], static_cast<uint32_t>(j / p.stages) & 1u, &dummy);
+      if (!ok) report(p.status);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      const uint32_t idesc = tile_idesc<T>(p.tn);
+      int stage = 0, as = 0, slot = 0;
+      uint32_t phase = 0, a_phase = 0, d_phase = 0;
+      for (int t = t0; ok && t < p.tiles; t += dt) {
+        if (!mbar_wait_bounded(&S.d_empty[slot], d_phase ^ 1u, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(slot * slot_cols(p.tn));
+        for (int k = k_begin; k < k_end; ++k) {
+          if (!mbar_wait_bounded(&S.full[stage], phase, abort) ||
+              !mbar_wait_bounded(&S.a_full[as], a_phase, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = a_base + static_cast<uint32_t>(as * kACols);
+          const uint32_t b = smem_addr(ring + stage * sbytes + kCodeBytes);
+#pragma unroll
+          for (int j = 0; j < kStepK / 16; ++j)
+            mma_ts(d, a + 8u * j, sw128_kmajor_desc(b + (j / 4) * p.tn * 128 + (j % 4) * 32), idesc,
+                   (k > k_begin || j > 0) ? 1u : 0u);
+          mma_commit(&S.empty[stage]);
+          mma_commit(&S.a_empty[as]);
+          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+          if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
+        }
+        if (!ok) break;
+        mma_commit(&S.d_full[slot]);
+        if (++slot == p.d_slots) { slot = 0; d_phase ^= 1u; }
+      }
+      mma_commit(&S.drain);  // every MMA is done before tensor memory is freed
+      int dummy = 0;
+      mbar_wait_bounded(&S.drain, 0, &dummy);
+      if (!ok) report(p.status);
+    }
+  } else if (warp < kDequantWarps) {
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    // the two 16-byte chunks of this thread's 32 bytes, under the 64-byte swizzle
+    const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
+    const uint32_t off0 = row * 64 + ((2u * half) ^ swz) * 16, off1 = row * 64 + ((2u * half + 1) ^ swz) * 16;
+    int stage = 0, as = 0;
+    uint32_t phase = 0, a_phase = 0;
+    for (int t = t0; ok && t < p.tiles; t += dt) {
+      const long long n = min(t / p.m_tiles * kTileN + row, p.N - 1);
+      const T* srow = static_cast<const T*>(p.scales) + n * p.groups;
+      const uint8_t* zrow = p.zeros ? p.zeros + n * p.groups : nullptr;
+      GroupChunk cur = {}, nxt = {};
+      int held = -1;  // first group of cur
+      for (int k = k_begin; k < k_end; ++k) {
+        const int g = (k * kStepK + half * 64) / p.group;
+        const int chunk = g & ~7;
+        if (chunk != held) {
+          if (chunk == held + 8 && held >= 0) cur = nxt;
+          else load_chunk<T>(cur, srow, zrow, chunk, p.groups);
+          held = chunk;
+          load_chunk<T>(nxt, srow, zrow, chunk + 8, p.groups);
+        }
+        if (!warp_wait(&S.full[stage], phase, abort)) { ok = false; break; }
+        const uint8_t* codes = ring + stage * sbytes;
+        const uint4 c0 = *reinterpret_cast<const uint4*>(codes + off0);
+        const uint4 c1 = *reinterpret_cast<const uint4*>(codes + off1);
+        Dequant<T> q;
+        uint32_t out[32];
+        q.set(chunk_scale2(cur, g & 7), zrow ? chunk_zero(cur, g & 7) : kInt4Zero);
+        q.word(c0.x, out);
+        q.word(c0.y, out + 4);
+        q.word(c0.z, out + 8);
+        q.word(c0.w, out + 12);
+        if (p.group == 32)  // the second 32 of the 64 k: the next group (g is even)
+          q.set(chunk_scale2(cur, (g + 1) & 7), zrow ? chunk_zero(cur, (g + 1) & 7) : kInt4Zero);
+        q.word(c1.x, out + 16);
+        q.word(c1.y, out + 20);
+        q.word(c1.z, out + 24);
+        q.word(c1.w, out + 28);
+        if (!warp_wait(&S.a_empty[as], a_phase ^ 1u, abort)) { ok = false; break; }
+        tc_fence_after();
+        tmem_st32(a_base + static_cast<uint32_t>(as * kACols + half * 32) + lane_base, out);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.a_full[as]);
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
+      }
+    }
+    if (!ok) report(p.status);
+  } else {
+    const int quad = warp & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    int slot = 0;
+    uint32_t d_phase = 0;
+    for (int t = t0; t < p.tiles; t += dt) {
+      const int m0 = t % p.m_tiles * p.tn, n = t / p.m_tiles * kTileN + quad * 32 + lane;
+      if (!warp_wait(&S.d_full[slot], d_phase, abort)) { ok = false; break; }
+      tc_fence_after();
+      const bool n_ok = n < p.N;
+      const float b = (p.bias && n_ok) ? to_f32(static_cast<const T*>(p.bias)[n]) : 0.0f;
+      float* part = reinterpret_cast<float*>(ring);  // splits > 1: the ring is drained
+      T* Y = static_cast<T*>(p.Y);
+      for (int c = 0; c < p.tn; c += 16) {
+        uint32_t r[16];
+        __syncwarp();
+        tmem_ld16(tmem + static_cast<uint32_t>(slot * slot_cols(p.tn) + c) + lane_base, r);
+        tmem_ld_wait();
+        if (p.splits > 1) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            part[(c + j) * kTileN + quad * 32 + lane] = __uint_as_float(r[j]);
+        } else if (n_ok) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const long long m = m0 + c + j;
+            if (m < p.M) Y[m * p.N + n] = from_f32<T>(__uint_as_float(r[j]) + b);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.d_empty[slot]);
+      if (++slot == p.d_slots) { slot = 0; d_phase ^= 1u; }
+    }
+    if (!ok) report(p.status);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
+  }
+  if (p.splits > 1) {
+    // one tile per cluster: every CTA's partial sums are in its shared memory
+    __syncwarp();
+    cluster_barrier_sync();
+    if (!S.abort) {
+      const int m0 = t0 % p.m_tiles * p.tn, n0 = t0 / p.m_tiles * kTileN;
+      const int c_begin = p.tn * split / p.splits, c_end = p.tn * (split + 1) / p.splits;
+      const uint32_t base = smem_addr(ring);
+      for (int i = c_begin * kTileN + static_cast<int>(threadIdx.x); i < c_end * kTileN; i += kThreads) {
+        const long long m = m0 + i / kTileN;
+        const int n = n0 + i % kTileN;
+        if (m >= p.M || n >= p.N) continue;
+        float v = 0.0f;
+        for (int r = 0; r < p.splits; ++r) v += ld_cluster_f32(mapa_shared(base, r) + 4u * i);
+        if (p.bias) v += to_f32(static_cast<const T*>(p.bias)[n]);
+        static_cast<T*>(p.Y)[m * p.N + n] = from_f32<T>(v);
+      }
+    }
+    __syncwarp();
+    cluster_barrier_sync();  // no CTA leaves while its sums are read
+  }
+}
+
+namespace {
+
+struct TilePlan {
+  int tn, stages, a_stages, d_slots, tmem_cols, splits, grid;
+  size_t smem;
+};
+
+TilePlan plan_tile(int M, int N, int K, int num_sms) {
+  TilePlan t;
+  const int n_tiles = (N + kTileN - 1) / kTileN;
+  const int steps = (K + kStepK - 1) / kStepK;
+  if (M <= 128) {
+    t.tn = (M + 15) / 16 * 16;
+  } else {
+    // the width that needs the least time in waves of one tile per SM
+    t.tn = 256;
+    long long best = -1;
+    for (int tn = 256; tn >= 64; tn -= 16) {
+      const int per_sm = tn <= 128 ? 2 : 1;
+      const long long tiles = static_cast<long long>((M + tn - 1) / tn) * n_tiles;
+      const long long waves = (tiles + num_sms * per_sm - 1) / (num_sms * per_sm);
+      const long long cost = waves * per_sm * (tn + 24);
+      if (best < 0 || cost < best) best = cost, t.tn = tn;
+    }
+  }
+  const long long tiles = static_cast<long long>((M + t.tn - 1) / t.tn) * n_tiles;
+  const int per_sm = t.tn <= 128 ? 2 : 1;
+  const int capacity = num_sms * per_sm;
+  t.splits = 1;
+  if (tiles < capacity) {
+    const int want = static_cast<int>(capacity / tiles);
+    const int most = steps / 2 > 1 ? steps / 2 : 1;  // two steps or more each
+    t.splits = want < 8 ? want : 8;
+    if (t.splits > most) t.splits = most;
+    if (t.splits < 1) t.splits = 1;
+  }
+  t.tmem_cols = per_sm == 2 ? 256 : 512;
+  t.d_slots = (t.splits == 1 && 2 * slot_cols(t.tn) + 2 * kACols <= t.tmem_cols) ? 2 : 1;
+  t.a_stages = (t.tmem_cols - t.d_slots * slot_cols(t.tn)) / kACols;
+  if (t.a_stages > kMaxA) t.a_stages = kMaxA;
+  const size_t budget = (per_sm == 2 ? 113 : 226) * 1024 - 1024 - sizeof(TileShared);
+  t.stages = static_cast<int>(budget / stage_bytes(t.tn));
+  if (t.stages > kMaxStages) t.stages = kMaxStages;
+  t.smem = static_cast<size_t>(t.stages) * stage_bytes(t.tn) + sizeof(TileShared) + 1024;
+  t.grid = t.splits > 1 ? static_cast<int>(tiles) * t.splits
+                        : static_cast<int>(tiles < capacity ? tiles : capacity);
+  return t;
+}
+
+template <typename T>
+cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
+  const Int4Weight& w = a.w;
+  const TilePlan t = plan_tile(a.M, w.N, w.K, num_sms);
+  CUtensorMap map_x, map_w;
+  if (!encode_tmap_2d(&map_x,
+                      w.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      a.X, w.K, a.M, static_cast<uint64_t>(w.K) * 2, 64,
+                      static_cast<uint32_t>(t.tn)) ||
+      !encode_tmap_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K / 2, w.N, w.K / 2,
+                      kStepK / 2, kTileN, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  TileArgs p;
+  p.scales = w.scales;
+  p.zeros = w.zeros;
+  p.bias = a.bias;
+  p.Y = a.Y;
+  p.status = a.status;
+  p.M = a.M;
+  p.N = w.N;
+  p.K = w.K;
+  p.group = w.group;
+  p.groups = w.groups;
+  p.tn = t.tn;
+  p.stages = t.stages;
+  p.a_stages = t.a_stages;
+  p.d_slots = t.d_slots;
+  p.tmem_cols = t.tmem_cols;
+  p.splits = t.splits;
+  p.m_tiles = (a.M + t.tn - 1) / t.tn;
+  const long long tiles = static_cast<long long>(p.m_tiles) * ((w.N + kTileN - 1) / kTileN);
+  if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
+  p.tiles = static_cast<int>(tiles);
+  p.steps = (w.K + kStepK - 1) / kStepK;
+  cudaError_t e = cudaFuncSetAttribute(int4_tile_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(226 * 1024));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(t.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = t.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = t.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = t.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, int4_tile_kernel<T>, map_x, map_w, p);
+}
+
+}  // namespace
+
+cudaError_t launch_int4_tile(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
+  return a.w.bf16 ? launch_typed<__nv_bfloat16>(a, num_sms, stream)
+                  : launch_typed<__half>(a, num_sms, stream);
+}
+
+}  // namespace i8mm
