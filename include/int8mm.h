@@ -41,6 +41,7 @@ extern "C" {
 typedef struct CUstream_st *int8mm_stream_t; /* the same type as cudaStream_t */
 
 #define INT8MM_MAX_K 65536
+#define INT8MM_MAX_ROWS 0x7FFFFF00 /* of M and N in the int4_* calls and the block norms */
 
 /* status codes */
 #define INT8MM_OK 0
@@ -332,7 +333,7 @@ int int8_linear_forward_noalloc(const void *X, int M, int K, const int8_t *Wq,
  *   zeros   uint8 [N, ceil(K/group)] whole numbers 0..15, or NULL: every zero point is 8
  * and they stand for W_hat[n,k] = scales[n,c] * (u[n,k] - zeros[n,c]), c = k / group.
  * group is 32, 64 or a multiple of 128 (else INT8MM_ERR_GROUP); it may exceed K, and the last
- * group of a row may be short.  K must be a multiple of 32, 1 <= N, K <= INT8MM_MAX_K.  The
+ * group of a row may be short.  K must be a multiple of 32, 1 <= K <= INT8MM_MAX_K, 1 <= M, N <= INT8MM_MAX_ROWS.  The
  * conventions at the top of this file hold for these calls too.
  */
 
@@ -368,6 +369,12 @@ int int4_dequant_weight(const uint8_t *codes, const void *scales, const uint8_t 
  *   dev_status [in/out] one int32 of device memory that receives a negative code if a bounded
  *              device-side wait gives up (zero it first), or NULL to not be told
  * No workspace: calls on different streams do not disturb each other.
+ * A NaN or an infinity in a row of X makes the results of that row NaN or infinite (which of the
+ * two is not said).  With few tokens the products are of the codes themselves; with more (M > 8,
+ * or activations beyond one SM's shared memory) of W_hat rounded to T, which has to be finite.
+ * As with int8_linear_forward, the weights may be read before the launch before this one on the
+ * stream is done: codes, scales and zeros must not be written by a kernel launched just before
+ * that lets its successors start early (int4_quant_weight and ordinary kernels do not).
  */
 int int4_linear_forward(const void *X, int M, int K, const uint8_t *codes, const void *scales,
                         const uint8_t *zeros, const void *bias, int N, int group, unsigned flags,

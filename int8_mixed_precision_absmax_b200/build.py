@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libint8mm.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm2.cu", "small.cu", "gemv.cu", "decode.cu", "stats.cu", "trace.cu",
-           "api_block.cu", "int4.cu", "int4_tile.cu", "norm.cu"]
+           "api_block.cu", "int4.cu", "int4_stream.cu", "int4_tile.cu", "norm.cu"]
 HEADERS = ["block.cuh", "codes.cuh", "kernels.cuh", "ptx.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -34,7 +34,7 @@ int launched(cudaError_t e) {
 
 int check_int4(int N, int K, int group, unsigned flags) {
   if (flags & ~INT8MM_BFLOAT16) return INT8MM_ERR_FLAGS;
-  if (N <= 0 || K <= 0 || K > INT8MM_MAX_K) return INT8MM_ERR_SHAPE;
+  if (N <= 0 || N > INT8MM_MAX_ROWS || K <= 0 || K > INT8MM_MAX_K) return INT8MM_ERR_SHAPE;
   if (K % 32 != 0) return INT8MM_ERR_ALIGN;
   if (group <= 0 || (group != 32 && group != 64 && group % 128 != 0)) return INT8MM_ERR_GROUP;
   return INT8MM_OK;
@@ -56,7 +56,7 @@ Int4Weight weight_of(const uint8_t* codes, const void* scales, const uint8_t* ze
 
 int check_norm(int M, int D, float eps, unsigned flags, unsigned allowed) {
   if (flags & ~allowed) return INT8MM_ERR_FLAGS;
-  if (M <= 0 || D <= 0 || D > INT8MM_MAX_K) return INT8MM_ERR_SHAPE;
+  if (M <= 0 || M > INT8MM_MAX_ROWS || D <= 0 || D > INT8MM_MAX_K) return INT8MM_ERR_SHAPE;
   if (D % 16 != 0) return INT8MM_ERR_ALIGN;
   if (!(eps >= 0.0f) || std::isinf(eps)) return INT8MM_ERR_VALUE;
   return INT8MM_OK;
@@ -95,7 +95,7 @@ int int4_linear_forward(const void* X, int M, int K, const uint8_t* codes, const
   if (!X || !codes || !scales || !Y) return INT8MM_ERR_NULL;
   int rc = check_int4(N, K, group, flags);
   if (rc) return rc;
-  if (M <= 0) return INT8MM_ERR_SHAPE;
+  if (M <= 0 || M > INT8MM_MAX_ROWS) return INT8MM_ERR_SHAPE;
   if (off16(X) || off16(codes) || off16(scales) || off16(zeros) || off16(bias) || off16(Y) ||
       (reinterpret_cast<uintptr_t>(dev_status) & 3u))
     return INT8MM_ERR_ALIGN;
@@ -107,9 +107,8 @@ int int4_linear_forward(const void* X, int M, int K, const uint8_t* codes, const
   a.Y = Y;
   a.M = M;
   a.status = dev_status;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launched(M > 8 ? launch_int4_tile(a, device_sm_count(), st)
-                        : launch_int4_linear(a, device_sm_count(), st));
+  return launched(
+      launch_int4_linear(a, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int int8_block_norm(const void* x, int M, int D, const void* weight, const void* bias, float eps,

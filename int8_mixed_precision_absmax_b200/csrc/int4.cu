@@ -1,4 +1,4 @@
-// int4.cu -- 4-bit weights with group scales: the quantizer, its inverse, and the product.
+// int4.cu -- 4-bit weights with group scales: the quantizer, its inverse, and which kernel multiplies.
 #include "block.cuh"
 
 namespace i8mm {
@@ -8,13 +8,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Sums or maxima over the `width` lanes of a warp segment (a power of two up to 32).
+// The maximum over the `width` lanes of a warp segment (a power of two up to 32).
 __device__ __forceinline__ float seg_max(float v, int width) {
   for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
 
@@ -133,57 +129,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// One warp per output channel and 4 tokens.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) int4_linear_kernel(const Int4LinearArgs a) {
-  constexpr int kTok = 4;
-  const int lane = threadIdx.x & 31;
-  const Int4Weight& w = a.w;
-  const T* scales = static_cast<const T*>(w.scales);
-  const T* X = static_cast<const T*>(a.X);
-  const T* bias = static_cast<const T*>(a.bias);
-  T* Y = static_cast<T*>(a.Y);
-  const int words = w.K / 8;
-  const long long tok_tiles = (a.M + kTok - 1) / kTok;
-  const long long total = tok_tiles * w.N;
-  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; i < total;
-       i += static_cast<long long>(gridDim.x) * kWarps) {
-    const long long n = i % w.N;
-    const long long m0 = i / w.N * kTok;
-    const uint32_t* row = reinterpret_cast<const uint32_t*>(w.codes) + n * words;
-    float acc[kTok] = {};
-    for (int j = lane; j < words; j += 32) {
-      const long long c = n * w.groups + j * 8 / w.group;
-      const float s = to_f32(scales[c]);
-      const float z = w.zeros ? static_cast<float>(w.zeros[c]) : static_cast<float>(kInt4Zero);
-      const uint32_t word = row[j];
-      float wv[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        wv[e] = (static_cast<float>((word >> (4 * int4_nibble(e))) & 15u) - z) * s;
-#pragma unroll
-      for (int t = 0; t < kTok; ++t) {
-        if (m0 + t < a.M) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(X + (m0 + t) * w.K + j * 8);
-          const uint32_t r[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 p = unpack2<T>(r[e]);
-            acc[t] = fmaf(p.x, wv[2 * e], acc[t]);
-            acc[t] = fmaf(p.y, wv[2 * e + 1], acc[t]);
-          }
-        }
-      }
-    }
-    const float b = bias ? to_f32(bias[n]) : 0.0f;
-#pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      const float v = warp_sum(acc[t]);
-      if (lane == 0 && m0 + t < a.M) Y[(m0 + t) * w.N + n] = from_f32<T>(v + b);
-    }
-  }
-}
-
 namespace {
 
 int blocks_for(long long work, int per_block, int num_sms) {
@@ -227,13 +172,8 @@ cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
-  const long long total = static_cast<long long>((a.M + 3) / 4) * a.w.N;
-  const int grid = blocks_for(total, kWarps, num_sms);
-  if (a.w.bf16)
-    int4_linear_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-  else
-    int4_linear_kernel<__half><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return int4_stream_fits(a.M, a.w.K) ? launch_int4_stream(a, num_sms, stream)
+                                      : launch_int4_tile(a, num_sms, stream);
 }
 
 }  // namespace i8mm
