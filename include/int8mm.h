@@ -370,7 +370,8 @@ int int4_dequant_weight(const uint8_t *codes, const void *scales, const uint8_t 
  *              device-side wait gives up (zero it first), or NULL to not be told
  * No workspace: calls on different streams do not disturb each other.
  * A NaN or an infinity in a row of X makes the results of that row NaN or infinite (which of the
- * two is not said).  With few tokens the products are of the codes themselves; with more (M > 8,
+ * two is not said); so may bfloat16 values of 2^112 and above, whose float32 sums can overflow.
+ * With few tokens the products are of the codes themselves; with more (M > 8,
  * or activations beyond one SM's shared memory) of W_hat rounded to T, which has to be finite.
  * As with int8_linear_forward, the weights may be read before the launch before this one on the
  * stream is done: codes, scales and zeros must not be written by a kernel launched just before

@@ -5,19 +5,18 @@
 //
 // Instructions, not bytes, are what such a kernel runs out of first (one SM must take in 56 weights
 // a cycle to keep up with HBM), so the unpacking is what everything is arranged around:
-//   - A code in the low bits of a 16-bit half is an fp16 subnormal, u 2^-24 (bits 0-3) or u 2^-20
+//   - fp16: a code in the low bits of a 16-bit half is a subnormal, u 2^-24 (bits 0-3) or u 2^-20
 //     (bits 4-7), which the tensor core multiplies exactly.  One AND gives two of them, so 8
 //     weights cost 4 ANDs and a shift, and no conversion.  Two accumulators keep the two powers
 //     apart and meet when a group is scaled: t = 16 lo + hi.
-//   - The zero point is taken out afterwards, with the sum of the group's activations that one more
-//     MMA against a constant gives (2^-20 sum X, in every row).
+//   - bf16 has no subnormals to spare (their products would be below float32's range): a code set
+//     into the mantissa of 128 reads as 128 + u, one AND-OR and a shift for two.
+//   - The zero point (and the 128) is taken out afterwards, with the sum of the group's activations
+//     that one more MMA against a constant gives in every row.
 //   - m16n8k16 with the weights as the 16-row operand: the 8 tokens are its columns.  The packing
 //     order puts neighbours into the two halves of a register, as X has them in memory; which k a
 //     lane takes is free as long as both operands agree: lane t of a quad takes the words 4q + t.
 // The group's scale meets the float32 sum of the group: the weights are never rounded.
-// bf16 activations become fp16 after a scaling of the token's row by a power of two that brings its
-// largest value to 2^14..2^15: exact but for values 2^-29 of the row's largest and below, whose
-// error is under 2^-39 of it, less than the float32 sums lose anyway.
 //
 // A block owns a range of 16-row units and takes them in pairs; its warps share the K axis in
 // chunks of 256 columns, each warp with a ring of its own that TMA fills (boxes of 16 rows x 128
@@ -51,22 +50,31 @@ struct StreamArgs {
   int32_t* status;
   int M, N, K, group, groups;
   int units, chunks, stages, xstride;
+  bool vector_groups;  // load_groups: a chunk's groups of a row are one aligned vector
 };
 
 struct StreamShared {
   uint64_t full[kMaxWarps][kMaxStages];
   uint64_t x_full;
-  uint32_t xmax[kMaxTok];
   int abort;
 };
 
+// d = a b + (first ? 0 : d)
+template <typename T>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                            uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                            uint32_t a3, uint32_t b0, uint32_t b1, bool first) {
+  const float c0 = first ? 0.0f : d[0], c1 = first ? 0.0f : d[1];
+  const float c2 = first ? 0.0f : d[2], c3 = first ? 0.0f : d[3];
+  if constexpr (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -74,12 +82,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
+// 16 bytes where `ok`; where not, the registers keep what they hold (zeros).
+__device__ __forceinline__ void lds128_if(uint4& v, uint32_t a, bool ok) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "r"(a), "r"(ok ? 1u : 0u));
 }
 
 // An untiled copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
@@ -107,8 +116,8 @@ __device__ __forceinline__ void load_groups(RowGroups<SUB>& r, const StreamArgs&
   const uint16_t* s = static_cast<const uint16_t*>(p.scales) + base;
   const uint8_t* z = ZP ? p.zeros + base : nullptr;
   // groups of one block's width lie side by side: one vector load where every row is aligned to it
-  if (kBlocks > 1 && p.group == 32 * SUB && p.groups % kBlocks == 0) {
-    const int g = k0 / p.group;
+  if (kBlocks > 1 && p.vector_groups) {
+    const int g = k0 / (32 * SUB);
     if constexpr (kBlocks == 8) {
       const uint4 v = *reinterpret_cast<const uint4*>(s + g);
       r.s[0] = v.x, r.s[1] = v.y, r.s[2] = v.z, r.s[3] = v.w;
@@ -144,6 +153,69 @@ __device__ __forceinline__ float scale_value(uint32_t word, int high) {
   return high ? v.y : v.x;
 }
 
+// One chunk of a pair of units (or of one, where not TWO) added to acc.  w: this lane's first word
+// under the swizzle; x: this lane's activations at the chunk's start; steps of 32 columns, 8 where
+// FULL.
+template <typename T, int SUB, bool ZP, bool TWO, bool FULL>
+__device__ __forceinline__ void add_chunk(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t w,
+                                          uint32_t x, bool tok_ok, int g, int steps) {
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr uint32_t kOne = kHalf ? 0x00100010u : 0x3F803F80u;  // 2^-20 or 1, twice
+  uint4 xv[2] = {};
+#pragma unroll
+  for (int j = 0; j < 8 / SUB; ++j) {
+    float lo[2][4], hi[2][4], sum[4];
+    if (!FULL && j * SUB >= steps) break;
+#pragma unroll
+    for (int e = 0; e < SUB; ++e) {
+      const int st = j * SUB + e;
+      if (FULL || st < steps) {
+        uint4& xr = xv[st & 1];
+        lds128_if(xr, x + 64u * st, tok_ok);
+        const uint32_t wo = w ^ (static_cast<uint32_t>(st) << 4);
+#pragma unroll
+        for (int i = 0; i < (TWO ? 2 : 1); ++i) {
+          const uint32_t wa = lds32(wo + i * kUnitBytes);
+          const uint32_t wb = lds32(wo + i * kUnitBytes + 1024);
+          if constexpr (kHalf) {
+            const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
+            mma_16x8x16<T>(lo[i], wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu,
+                           wb8 & 0x000F000Fu, xr.x, xr.z, e == 0);
+            mma_16x8x16<T>(hi[i], wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u,
+                           wb8 & 0x00F000F0u, xr.y, xr.w, e == 0);
+          } else {
+            constexpr uint32_t k128 = 0x43004300u;
+            mma_16x8x16<T>(lo[i], (wa & 0x000F000Fu) | k128, (wb & 0x000F000Fu) | k128,
+                           (wa >> 8 & 0x000F000Fu) | k128, (wb >> 8 & 0x000F000Fu) | k128, xr.x,
+                           xr.z, e == 0);
+            mma_16x8x16<T>(lo[i], (wa >> 4 & 0x000F000Fu) | k128, (wb >> 4 & 0x000F000Fu) | k128,
+                           (wa >> 12 & 0x000F000Fu) | k128, (wb >> 12 & 0x000F000Fu) | k128, xr.y,
+                           xr.w, false);
+          }
+        }
+        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr.x, xr.z, e == 0);
+        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr.y, xr.w, false);
+      }
+    }
+    // the block's scales: rows g, g + 8, 16 + g, 24 + g, held by the lanes of those numbers
+#pragma unroll
+    for (int r = 0; r < (TWO ? 4 : 2); ++r) {
+      const uint32_t sw = __shfl_sync(~0u, rg.s[j / 2], g + 8 * r);
+      const float s = scale_value<T>(sw, j & 1);
+      float z = kInt4Zero;
+      if (ZP)
+        z = static_cast<float>(__shfl_sync(~0u, rg.z[j / 4], g + 8 * r) >> (8 * (j & 3)) & 0xFFu);
+      if (!kHalf) z += 128.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = r / 2, d = 2 * (r & 1) + h;
+        const float v = kHalf ? fmaf(lo[i][d], 16.0f, hi[i][d]) : lo[i][d];
+        acc[i][d] = fmaf(s, fmaf(-z, sum[h], v), acc[i][d]);
+      }
+    }
+  }
+}
+
 }  // namespace
 
 template <typename T, int SUB, bool ZP>
@@ -164,7 +236,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     for (int w = 0; w < warps; ++w)
       for (int s = 0; s < p.stages; ++s) mbar_init(&S.full[w][s], 1);
     mbar_init(&S.x_full, 1);
-    for (int m = 0; m < kMaxTok; ++m) S.xmax[m] = 0;
     S.abort = 0;
     fence_mbarrier_init();
     prefetch_tmap(&map_w);
@@ -175,17 +246,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   const int u0 = static_cast<int>(static_cast<long long>(p.units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<long long>(p.units) * (blockIdx.x + 1) / gridDim.x);
   const int pairs = (u1 - u0 + 1) / 2;
-  // Chunks go round the warps, on from pair to pair: chunk c of pair q to warp (q chunks + c) % warps.
-  const int step = p.chunks % warps;
+  // Chunks go round the warps, on from pair to pair: warp, warp + warps, ... of all in a row.
   uint8_t* my_ring = ring + static_cast<size_t>(warp) * p.stages * kStageBytes;
   uint64_t* my_full = S.full[warp];
 
   int fp = 0, fc = warp, f_stage = 0, issued = 0;  // the next chunk to request
-  auto settle = [&](int& q, int& c) {  // past the pair's last chunk: on to the next pair's first
-    while (c >= p.chunks && q < pairs) {
+  auto settle = [&](int& q, int& c) {  // past the pair's last chunk: into the next pair
+    while (c >= p.chunks) {
+      c -= p.chunks;
       ++q;
-      int first = warp - static_cast<int>(static_cast<long long>(q) * step % warps);
-      c = first < 0 ? first + warps : first;
     }
   };
   auto request = [&]() {
@@ -220,36 +289,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K, row_bytes, &S.x_full);
   }
   bool ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    // the largest finite magnitude of each row, then the rows as fp16
-    for (int m = 0; m < p.M; ++m) {
-      uint32_t most = 0;
-      for (int i = threadIdx.x; i < p.K / 2; i += blockDim.x) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(xs + static_cast<size_t>(m) * p.xstride + 4 * i);
-        const uint32_t a = v & 0x7FFFu, b = v >> 16 & 0x7FFFu;
-        if (a < 0x7F80u) most = max(most, a);
-        if (b < 0x7F80u) most = max(most, b);
-      }
-      most = __reduce_max_sync(~0u, most);
-      if (lane == 0) atomicMax(&S.xmax[m], most);
-    }
-    __syncthreads();
-    for (int m = 0; m < p.M; ++m) {
-      const int e = static_cast<int>(S.xmax[m] >> 7) - 127 - 14;  // the largest becomes 2^14 ..
-      // 2^-e (-113 <= -e <= 141) in two factors
-      const float f1 = __int_as_float((127 - e / 2) << 23), f2 = __int_as_float((127 - (e - e / 2)) << 23);
-      for (int i = threadIdx.x; i < p.K / 2; i += blockDim.x) {
-        uint32_t* v = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(m) * p.xstride + 4 * i);
-        const float2 f = unpack2<__nv_bfloat16>(*v);
-        *v = pack2<__half>(f.x * f1 * f2, f.y * f1 * f2);
-      }
-    }
-    __syncthreads();
-  }
 
   const uint32_t x_lane = smem_addr(xs) + static_cast<uint32_t>(g) * p.xstride + 16u * t;
   const bool tok_ok = g < p.M;
-  const uint32_t w_lane = smem_addr(my_ring) + static_cast<uint32_t>(g) * 128 + 4u * t;
+  // a lane's words of row g: 16-byte piece st of the row lies at piece st ^ g
+  const uint32_t w_lane = smem_addr(my_ring) + static_cast<uint32_t>(g) * (128 + 16) + 4u * t;
   int stage = 0;
   uint32_t phase = 0;
   for (int pair = 0; pair < pairs; ++pair) {
@@ -262,48 +306,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&my_full[stage], phase, abort));
       if (ok) {
         const int k0 = c * kChunkK;
-        const int steps = min(8, (p.K - k0) / 32);
-        const uint32_t w_st = w_lane + static_cast<uint32_t>(stage) * kStageBytes;
-        const uint32_t x_st = x_lane + 2u * k0;
-#pragma unroll
-        for (int j = 0; j < 8 / SUB; ++j) {
-          float lo[2][4] = {}, hi[2][4] = {}, sum[4] = {};
-#pragma unroll
-          for (int e = 0; e < SUB; ++e) {
-            const int st = j * SUB + e;
-            if (st < steps) {
-              const uint4 x = tok_ok ? lds128(x_st + 64u * st) : make_uint4(0, 0, 0, 0);
-              const uint32_t wo = (static_cast<uint32_t>(st) ^ static_cast<uint32_t>(g)) * 16;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t wa = lds32(w_st + i * kUnitBytes + wo);
-                const uint32_t wb = lds32(w_st + i * kUnitBytes + 1024 + wo);
-                const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
-                mma_16x8x16(lo[i], wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu,
-                            wb8 & 0x000F000Fu, x.x, x.z);
-                mma_16x8x16(hi[i], wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u,
-                            wb8 & 0x00F000F0u, x.y, x.w);
-              }
-              constexpr uint32_t kOne = 0x00100010u;  // 2^-20, twice
-              mma_16x8x16(sum, kOne, kOne, kOne, kOne, x.x, x.z);
-              mma_16x8x16(sum, kOne, kOne, kOne, kOne, x.y, x.w);
-            }
-          }
-          // the block's scales: rows g, g + 8, 16 + g, 24 + g, held by the lanes of those numbers
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t sw = __shfl_sync(~0u, cur.s[j / 2], g + 8 * r);
-            const float s = scale_value<T>(sw, j & 1);
-            float z = kInt4Zero;
-            if (ZP) z = static_cast<float>(__shfl_sync(~0u, cur.z[j / 4], g + 8 * r) >> (8 * (j & 3)) & 0xFFu);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = r / 2, d = 2 * (r & 1) + h;
-              const float v = fmaf(lo[i][d], 16.0f, hi[i][d]);
-              acc[i][d] = fmaf(s, fmaf(-z, sum[h], v), acc[i][d]);
-            }
-          }
-        }
+        const int steps = (p.K - k0) / 32;
+        const uint32_t w = w_lane + static_cast<uint32_t>(stage) * kStageBytes, x = x_lane + 2u * k0;
+        const bool two = u0 + 2 * pair + 1 < u1;
+        if (two && steps >= 8)
+          add_chunk<T, SUB, ZP, true, true>(acc, cur, w, x, tok_ok, g, 8);
+        else if (steps >= 8)
+          add_chunk<T, SUB, ZP, false, true>(acc, cur, w, x, tok_ok, g, 8);
+        else
+          add_chunk<T, SUB, ZP, true, false>(acc, cur, w, x, tok_ok, g, steps);
       }
       __syncwarp();
       if (ok) request();
@@ -330,9 +341,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (n >= row_end) continue;
       float v = 0.0f;
       for (int w = 0; w < warps; ++w) v += all[w * 32 * p.M + i];
-      int e = 20;  // the sums are of 2^-20 u X
-      if (std::is_same<T, __nv_bfloat16>::value) e += static_cast<int>(S.xmax[m] >> 7) - 127 - 14;
-      v = ldexpf(v, e);
+      if (std::is_same<T, __half>::value) v *= 1048576.0f;  // the sums are of 2^-20 u X
       if (p.bias) v += to_f32(static_cast<const T*>(p.bias)[n]);
       static_cast<T*>(p.Y)[static_cast<size_t>(m) * p.N + n] = from_f32<T>(v);
     }
@@ -433,6 +442,8 @@ cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_
   p.chunks = (w.K + kChunkK - 1) / kChunkK;
   p.stages = s.stages;
   p.xstride = s.xstride;
+  const int blocks = w.group == 32 ? 8 : w.group == 64 ? 4 : 2;  // groups in a chunk
+  p.vector_groups = w.group <= 128 && w.groups % blocks == 0;
   const int grid = p.units < num_sms ? p.units : num_sms;
   if (w.bf16)
     return w.zeros ? launch_sub<__nv_bfloat16, true>(map, p, s, grid, stream)
