@@ -99,7 +99,7 @@ cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
                                 cudaStream_t stream);
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
 // few tokens (int4_stream.cu): up to 8, as long as their activations fit into shared memory
-bool int4_stream_fits(int M, int K);
+bool int4_stream_fits(int M, int K, int group);
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
 // more (int4_tile.cu): tcgen05
 cudaError_t launch_int4_tile(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);

@@ -77,18 +77,17 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-// 16 bytes where `ok`; where not, the registers keep what they hold (zeros).
-__device__ __forceinline__ void lds128_if(uint4& v, uint32_t a, bool ok) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "r"(a), "r"(ok ? 1u : 0u));
+// W consecutive 32-bit words of shared memory.
+template <int W>
+__device__ __forceinline__ void lds(uint32_t (&v)[W], uint32_t a) {
+  if constexpr (W == 1)
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a));
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+  else
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(a));
 }
 
 // An untiled copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
@@ -153,58 +152,72 @@ __device__ __forceinline__ float scale_value(uint32_t word, int high) {
   return high ? v.y : v.x;
 }
 
-// One chunk of a pair of units (or of one, where not TWO) added to acc.  w: this lane's first word
-// under the swizzle; x: this lane's activations at the chunk's start; steps of 32 columns, 8 where
-// FULL.
-template <typename T, int SUB, bool ZP, bool TWO, bool FULL>
-__device__ __forceinline__ void add_chunk(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t w,
-                                          uint32_t x, bool tok_ok, int g, int steps) {
+// Words a lane takes at once: of 32 kWords<SUB> columns, lane t of a quad takes those from
+// 8 kWords t on (columns of one group only).
+template <int SUB>
+constexpr int kWords = SUB < 4 ? SUB : 4;
+
+// One chunk of a pair of units (or of one, where not TWO) added to acc.  row: this lane's row g of
+// the first unit in the stage, swz its swizzle (the row's number << 4) and x its activations at the
+// chunk's start; src: the lane that holds row g's scales.
+template <typename T, int SUB, bool ZP, bool TWO>
+__device__ __forceinline__ void add_chunk(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t row,
+                                          uint32_t swz, uint32_t x, int t, int src) {
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr uint32_t kOne = kHalf ? 0x00100010u : 0x3F803F80u;  // 2^-20 or 1, twice
-  uint4 xv[2] = {};
+  constexpr int W = kWords<SUB>;
+  const uint32_t x_t = x + 16u * W * t;
 #pragma unroll
   for (int j = 0; j < 8 / SUB; ++j) {
     float lo[2][4], hi[2][4], sum[4];
-    if (!FULL && j * SUB >= steps) break;
 #pragma unroll
-    for (int e = 0; e < SUB; ++e) {
-      const int st = j * SUB + e;
-      if (FULL || st < steps) {
-        uint4& xr = xv[st & 1];
-        lds128_if(xr, x + 64u * st, tok_ok);
-        const uint32_t wo = w ^ (static_cast<uint32_t>(st) << 4);
+    for (int e = 0; e < SUB / W; ++e) {
+      const int k = (j * SUB + e * W) * 32;  // first column
+      // bytes k/2 + 4 W t of the row, 16-byte pieces swizzled
+      const uint32_t at = row + ((static_cast<uint32_t>(k / 2) + 4u * W * t) ^ swz);
+      uint32_t wa[2][W], wb[2][W];
+#pragma unroll
+      for (int i = 0; i < (TWO ? 2 : 1); ++i) {
+        lds<W>(wa[i], at + i * kUnitBytes);
+        lds<W>(wb[i], at + i * kUnitBytes + 1024);
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const bool first = e == 0 && w == 0;
+        uint32_t xr[4];
+        lds<4>(xr, x_t + 2u * k + 16u * w);
 #pragma unroll
         for (int i = 0; i < (TWO ? 2 : 1); ++i) {
-          const uint32_t wa = lds32(wo + i * kUnitBytes);
-          const uint32_t wb = lds32(wo + i * kUnitBytes + 1024);
+          const uint32_t a = wa[i][w], b = wb[i][w];
           if constexpr (kHalf) {
-            const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
-            mma_16x8x16<T>(lo[i], wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu,
-                           wb8 & 0x000F000Fu, xr.x, xr.z, e == 0);
-            mma_16x8x16<T>(hi[i], wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u,
-                           wb8 & 0x00F000F0u, xr.y, xr.w, e == 0);
+            // the activations' words lie in the order 0, 2, 1, 3
+            const uint32_t a8 = a >> 8, b8 = b >> 8;
+            mma_16x8x16<T>(lo[i], a & 0x000F000Fu, b & 0x000F000Fu, a8 & 0x000F000Fu,
+                           b8 & 0x000F000Fu, xr[0], xr[1], first);
+            mma_16x8x16<T>(hi[i], a & 0x00F000F0u, b & 0x00F000F0u, a8 & 0x00F000F0u,
+                           b8 & 0x00F000F0u, xr[2], xr[3], first);
           } else {
             constexpr uint32_t k128 = 0x43004300u;
-            mma_16x8x16<T>(lo[i], (wa & 0x000F000Fu) | k128, (wb & 0x000F000Fu) | k128,
-                           (wa >> 8 & 0x000F000Fu) | k128, (wb >> 8 & 0x000F000Fu) | k128, xr.x,
-                           xr.z, e == 0);
-            mma_16x8x16<T>(lo[i], (wa >> 4 & 0x000F000Fu) | k128, (wb >> 4 & 0x000F000Fu) | k128,
-                           (wa >> 12 & 0x000F000Fu) | k128, (wb >> 12 & 0x000F000Fu) | k128, xr.y,
-                           xr.w, false);
+            mma_16x8x16<T>(lo[i], (a & 0x000F000Fu) | k128, (b & 0x000F000Fu) | k128,
+                           (a >> 4 & 0x000F000Fu) | k128, (b >> 4 & 0x000F000Fu) | k128, xr[0],
+                           xr[1], first);
+            mma_16x8x16<T>(lo[i], (a >> 8 & 0x000F000Fu) | k128, (b >> 8 & 0x000F000Fu) | k128,
+                           (a >> 12 & 0x000F000Fu) | k128, (b >> 12 & 0x000F000Fu) | k128, xr[2],
+                           xr[3], false);
           }
         }
-        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr.x, xr.z, e == 0);
-        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr.y, xr.w, false);
+        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[0], xr[1], first);
+        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[2], xr[3], false);
       }
     }
-    // the block's scales: rows g, g + 8, 16 + g, 24 + g, held by the lanes of those numbers
+    // the block's scales: rows g and g + 8 of each unit
 #pragma unroll
     for (int r = 0; r < (TWO ? 4 : 2); ++r) {
-      const uint32_t sw = __shfl_sync(~0u, rg.s[j / 2], g + 8 * r);
+      const uint32_t sw = __shfl_sync(~0u, rg.s[j / 2], src + 8 * r);
       const float s = scale_value<T>(sw, j & 1);
       float z = kInt4Zero;
       if (ZP)
-        z = static_cast<float>(__shfl_sync(~0u, rg.z[j / 4], g + 8 * r) >> (8 * (j & 3)) & 0xFFu);
+        z = static_cast<float>(__shfl_sync(~0u, rg.z[j / 4], src + 8 * r) >> (8 * (j & 3)) & 0xFFu);
       if (!kHalf) z += 128.0f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -288,12 +301,32 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       bulk_load(xs + static_cast<size_t>(m) * p.xstride,
                 static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K, row_bytes, &S.x_full);
   }
+  // zeros behind the rows, up to the end of the last chunk
+  const int pad = p.chunks * kChunkK / 8 - p.K / 8;  // 16-byte pieces
+  for (int i = threadIdx.x; i < pad * p.M; i += blockDim.x)
+    *reinterpret_cast<uint4*>(xs + static_cast<size_t>(i / pad) * p.xstride + 2 * p.K + i % pad * 16) =
+        make_uint4(0, 0, 0, 0);
   bool ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
+  if constexpr (std::is_same<T, __half>::value) {
+    // The two operand words of an MMA are a register pair: the words 0 and 2 of 16 bytes (the low
+    // nibbles' columns), then 1 and 3.
+    for (int m = 0; m < p.M; ++m) {
+      for (int i = threadIdx.x; i < p.K / 8; i += blockDim.x) {
+        uint32_t* v = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(m) * p.xstride) + 4 * i;
+        const uint32_t one = v[1], two = v[2];
+        v[1] = two;
+        v[2] = one;
+      }
+    }
+  }
+  __syncthreads();
 
-  const uint32_t x_lane = smem_addr(xs) + static_cast<uint32_t>(g) * p.xstride + 16u * t;
-  const bool tok_ok = g < p.M;
-  // a lane's words of row g: 16-byte piece st of the row lies at piece st ^ g
-  const uint32_t w_lane = smem_addr(my_ring) + static_cast<uint32_t>(g) * (128 + 16) + 4u * t;
+  // Row g of an MMA is row `gr` of the unit, the bits of g reversed: the rows that read shared
+  // memory together then differ in the swizzle's high bits (conflict-free for 4, 8 and 16 bytes).
+  const int gr = (g & 1) << 2 | (g & 2) | g >> 2;
+  // columns past the last token repeat it: their results are not kept
+  const uint32_t x_lane = smem_addr(xs) + static_cast<uint32_t>(min(g, p.M - 1)) * p.xstride;
+  const uint32_t w_lane = smem_addr(my_ring) + static_cast<uint32_t>(gr) * 128;
   int stage = 0;
   uint32_t phase = 0;
   for (int pair = 0; pair < pairs; ++pair) {
@@ -305,16 +338,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (nq < pairs) load_groups<SUB, ZP>(nxt, p, (u0 + 2 * nq) * kUnitRows + lane, nc * kChunkK);
       if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&my_full[stage], phase, abort));
       if (ok) {
-        const int k0 = c * kChunkK;
-        const int steps = (p.K - k0) / 32;
-        const uint32_t w = w_lane + static_cast<uint32_t>(stage) * kStageBytes, x = x_lane + 2u * k0;
-        const bool two = u0 + 2 * pair + 1 < u1;
-        if (two && steps >= 8)
-          add_chunk<T, SUB, ZP, true, true>(acc, cur, w, x, tok_ok, g, 8);
-        else if (steps >= 8)
-          add_chunk<T, SUB, ZP, false, true>(acc, cur, w, x, tok_ok, g, 8);
+        const uint32_t w = w_lane + static_cast<uint32_t>(stage) * kStageBytes;
+        const uint32_t x = x_lane + 2u * kChunkK * c;
+        if (u0 + 2 * pair + 1 < u1)
+          add_chunk<T, SUB, ZP, true>(acc, cur, w, 16u * gr, x, t, gr);
         else
-          add_chunk<T, SUB, ZP, true, false>(acc, cur, w, x, tok_ok, g, steps);
+          add_chunk<T, SUB, ZP, false>(acc, cur, w, 16u * gr, x, t, gr);
       }
       __syncwarp();
       if (ok) request();
@@ -329,7 +358,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       const int m = 2 * t + h;
       if (m < p.M) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mine[m * 32 + g + 8 * r] = acc[r / 2][2 * (r & 1) + h];
+        for (int r = 0; r < 4; ++r) mine[m * 32 + gr + 8 * r] = acc[r / 2][2 * (r & 1) + h];
       }
     }
     __syncthreads();
@@ -364,9 +393,11 @@ struct StreamPlan {
 };
 
 // Fits where the activations of all tokens leave room for two stages of 8 warps.
-bool plan_stream(int M, int K, StreamPlan& s) {
+bool plan_stream(int M, int K, int group, StreamPlan& s) {
   if (M > kMaxTok) return false;
-  s.xstride = K * 2 + 64;  // K * 2 is a multiple of 64; the pad sets two tokens' quads apart
+  // a row up to its last chunk's end, and a pad that sets the quads of two tokens apart (64 bytes
+  // where a lane reads every fourth 16 bytes, otherwise 16)
+  s.xstride = (K + kChunkK - 1) / kChunkK * kChunkK * 2 + (group == 32 ? 64 : 16);
   for (int warps = kMaxWarps; warps >= 8; warps /= 2) {
     const size_t fixed = 1024 + sizeof(StreamShared) + static_cast<size_t>(M) * s.xstride +
                          static_cast<size_t>(2) * warps * 32 * M * sizeof(float);
@@ -413,16 +444,16 @@ cudaError_t launch_sub(const CUtensorMap& map, const StreamArgs& p, const Stream
 
 }  // namespace
 
-bool int4_stream_fits(int M, int K) {
+bool int4_stream_fits(int M, int K, int group) {
   StreamPlan s;
-  return plan_stream(M, K, s);
+  return plan_stream(M, K, group, s);
 }
 
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
   const Int4Weight& w = a.w;
   StreamPlan s;
   CUtensorMap map;
-  if (!plan_stream(a.M, w.K, s) ||
+  if (!plan_stream(a.M, w.K, w.group, s) ||
       !encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K / 2, w.N, w.K / 2,
                       kChunkK / 2, kUnitRows))
     return cudaErrorInvalidValue;
