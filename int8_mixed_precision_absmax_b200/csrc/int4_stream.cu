@@ -3,26 +3,40 @@
 //
 //   Y[m,n] = T( sum_c s[n,c] ( sum_{k in c} u[n,k] X[m,k] - z[n,c] sum_{k in c} X[m,k] ) + bias[n] )
 //
-// Instructions, not bytes, are what such a kernel runs out of first (one SM must take in 56 weights
-// a cycle to keep up with HBM), so the unpacking is what everything is arranged around:
+// Instructions, not bytes, are what such a kernel runs out of first: one SM must take in 56 weights
+// a cycle to keep up with HBM, and its logic unit gives 64 results a cycle.  So the codes go into
+// mma.sync almost as they lie in memory, the weights as the 16-row operand and the activations as
+// the 8 columns, in one of two ways.
+//
+// One or two tokens (kDigits): u8 x s8 MMAs.  One AND makes 4 operands of a word's low nibbles,
+// another 4 of its high nibbles (16 u; two accumulators keep the two apart and meet when a group
+// is scaled: 16 lo + hi).  The activations are written in three digits,
+//   X = 2^e (65536 d2 + 256 d1 + d0),  d in -128..127,  2^(e+21) near the largest |X| of 256 columns
+// a fixed-point number of 23 bits, off by at most 2^-21 of that largest value (a float32 sum of its
+// products loses as much).  Three columns are one token, so all sums of a group are whole numbers
+// and exact; scaled, they are summed in float32 column by column.  256 columns that hold a NaN or an
+// infinity have no such numbers: the token's results are NaN.
+//
+// Three to 8 tokens: 16-bit MMAs (the digits of more tokens would need more MMAs than the HBM rate
+// leaves time for: three tokens of 5120 x 13824 took 40 us, against 17).
 //   - fp16: a code in the low bits of a 16-bit half is a subnormal, u 2^-24 (bits 0-3) or u 2^-20
 //     (bits 4-7), which the tensor core multiplies exactly.  One AND gives two of them, so 8
 //     weights cost 4 ANDs and a shift, and no conversion.  Two accumulators keep the two powers
 //     apart and meet when a group is scaled: t = 16 lo + hi.
 //   - bf16 has no subnormals to spare (their products would be below float32's range): a code set
 //     into the mantissa of 128 reads as 128 + u, one AND-OR and a shift for two.
-//   - The zero point (and the 128) is taken out afterwards, with the sum of the group's activations
-//     that one more MMA against a constant gives in every row.
-//   - m16n8k16 with the weights as the 16-row operand: the 8 tokens are its columns.  The packing
-//     order puts neighbours into the two halves of a register, as X has them in memory; which k a
-//     lane takes is free as long as both operands agree: lane t of a quad takes the words 4q + t.
-// The group's scale meets the float32 sum of the group: the weights are never rounded.
+//
+// Either way the zero point (and the 128) is taken out with the sum of the group's activations,
+// which one more MMA against a constant gives in every row, and the group's scale meets the float32
+// sum of the group: the weights are never rounded.  Which k a lane takes is free as long as both
+// operands agree: lane t of a quad takes neighbouring words of its row.
 //
 // A block owns a range of 16-row units and takes them in pairs; its warps share the K axis in
 // chunks of 256 columns, each warp with a ring of its own that TMA fills (boxes of 16 rows x 128
-// bytes, 128-byte swizzle: the 32-bit reads of a quad's words hit 32 banks).  The first chunks are
-// requested before the wait for the previous launch.  Partial sums of a pair meet in shared
-// memory, in the order of the warps.
+// bytes, 128-byte swizzle).  The first chunks are requested before the wait for the previous
+// launch.  The warp that takes a chunk of the first pair brings that chunk's activations into shared
+// memory for all pairs, so nothing waits for the whole of X.  Partial sums meet in shared memory
+// every `batch` pairs, in an order that does not change.
 #include <type_traits>
 
 #include "block.cuh"
@@ -39,7 +53,7 @@ constexpr int kChunkK = 256;                        // columns of a chunk: 128 b
 constexpr int kUnitBytes = kUnitRows * kChunkK / 2;
 constexpr int kStageBytes = 2 * kUnitBytes;         // a pair of units
 constexpr int kMaxWarps = 16, kMaxStages = 4;
-constexpr size_t kSmemMost = 227 * 1024;
+constexpr size_t kSmemMost = 226 * 1024;  // of an SM, for one block or for two
 
 struct StreamArgs {
   const void* X;
@@ -49,15 +63,26 @@ struct StreamArgs {
   void* Y;
   int32_t* status;
   int M, N, K, group, groups;
-  int units, chunks, stages, xstride;
+  int units, chunks, stages, xstride, batch;
   bool vector_groups;  // load_groups: a chunk's groups of a row are one aligned vector
 };
 
 struct StreamShared {
   uint64_t full[kMaxWarps][kMaxStages];
-  uint64_t x_full;
+  uint64_t x_full;                           // 16-bit operands: the activations are there
+  uint64_t x_ready[INT8MM_MAX_K / kChunkK];  // a chunk's activations are operands
   int abort;
 };
+
+// d = a b + (first ? c : d): unsigned by signed bytes, 32-bit sums.
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, bool first, int c) {
+  const int c0 = first ? c : d[0], c1 = first ? c : d[1], c2 = first ? c : d[2], c3 = first ? c : d[3];
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
+}
 
 // d = a b + (first ? 0 : d)
 template <typename T>
@@ -152,72 +177,139 @@ __device__ __forceinline__ float scale_value(uint32_t word, int high) {
   return high ? v.y : v.x;
 }
 
-// Words a lane takes at once: of 32 kWords<SUB> columns, lane t of a quad takes those from
-// 8 kWords t on (columns of one group only).
-template <int SUB>
-constexpr int kWords = SUB < 4 ? SUB : 4;
+// A whole number below 2^22 added to these bits reads as the float kMagic plus that number.
+constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagic = 12582912.0f;
 
-// One chunk of a pair of units (or of one, where not TWO) added to acc.  row: this lane's row g of
-// the first unit in the stage, swz its swizzle (the row's number << 4) and x its activations at the
-// chunk's start; src: the lane that holds row g's scales.
+// A whole number below 2^23, off the slow conversion pipe.
+__device__ __forceinline__ float small_float(uint32_t v) {
+  return __uint_as_float(v | 0x4B000000u) - 8388608.0f;
+}
+
+// One chunk of a pair of units (or of one, where not TWO) added to acc.  row: this lane's row of the
+// first unit in the stage, swz its swizzle (the row's number << 4) and x its column's digits at the
+// chunk's start; src: the lane that holds the row's scales.
+//
+// SUB words a lane takes at once: of 32 SUB columns (of one group), lane t of a quad takes those
+// from 8 SUB t on.  Two words and their digits are two MMAs, for the low and the high nibbles;
+// the digits lie in that order.  A single word is one MMA, low and high nibbles its two halves of k.
 template <typename T, int SUB, bool ZP, bool TWO>
-__device__ __forceinline__ void add_chunk(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t row,
-                                          uint32_t swz, uint32_t x, int t, int src) {
-  constexpr bool kHalf = std::is_same<T, __half>::value;
-  constexpr uint32_t kOne = kHalf ? 0x00100010u : 0x3F803F80u;  // 2^-20 or 1, twice
-  constexpr int W = kWords<SUB>;
-  const uint32_t x_t = x + 16u * W * t;
+__device__ __forceinline__ void add_chunk_digits(float (&acc)[2][4], const RowGroups<SUB>& rg,
+                                                 uint32_t row, uint32_t swz, uint32_t x, int t,
+                                                 int src) {
+  constexpr uint32_t kOnes = 0x01010101u, kLow = 0x0F0F0F0Fu, kHigh = 0xF0F0F0F0u;
+  constexpr int U = TWO ? 2 : 1;
 #pragma unroll
   for (int j = 0; j < 8 / SUB; ++j) {
-    float lo[2][4], hi[2][4], sum[4];
+    int lo[2][4], hi[2][4], sum[4];
+    // columns 32 SUB j + 8 SUB t on: bytes 16 SUB j + 4 SUB t of the row, 16-byte pieces swizzled
+    const uint32_t at = row + ((16u * SUB * j + 4u * SUB * t) ^ swz);
+    const uint32_t xj = x + 32u * SUB * j + 8u * SUB * t;
+    uint32_t wa[2][SUB], wb[2][SUB];
 #pragma unroll
-    for (int e = 0; e < SUB / W; ++e) {
-      const int k = (j * SUB + e * W) * 32;  // first column
-      // bytes k/2 + 4 W t of the row, 16-byte pieces swizzled
-      const uint32_t at = row + ((static_cast<uint32_t>(k / 2) + 4u * W * t) ^ swz);
-      uint32_t wa[2][W], wb[2][W];
+    for (int i = 0; i < U; ++i) {
+      lds<SUB>(wa[i], at + i * kUnitBytes);
+      lds<SUB>(wb[i], at + i * kUnitBytes + 1024);
+    }
+    if constexpr (SUB == 1) {
+      uint32_t xr[2];
+      lds<2>(xr, xj);
 #pragma unroll
-      for (int i = 0; i < (TWO ? 2 : 1); ++i) {
-        lds<W>(wa[i], at + i * kUnitBytes);
-        lds<W>(wb[i], at + i * kUnitBytes + 1024);
-      }
+      for (int i = 0; i < U; ++i)
+        mma_u8s8(hi[i], wa[i][0] & kLow, wb[i][0] & kLow, wa[i][0] >> 4 & kLow, wb[i][0] >> 4 & kLow,
+                 xr[0], xr[1], true, kMagicBits);
+      mma_u8s8(sum, kOnes, kOnes, kOnes, kOnes, xr[0], xr[1], true, kMagicBits);
+    } else {
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const bool first = e == 0 && w == 0;
+      for (int w = 0; w < SUB; w += 2) {
         uint32_t xr[4];
-        lds<4>(xr, x_t + 2u * k + 16u * w);
+        lds<4>(xr, xj + 8u * w);
 #pragma unroll
-        for (int i = 0; i < (TWO ? 2 : 1); ++i) {
-          const uint32_t a = wa[i][w], b = wb[i][w];
-          if constexpr (kHalf) {
-            // the activations' words lie in the order 0, 2, 1, 3
-            const uint32_t a8 = a >> 8, b8 = b >> 8;
-            mma_16x8x16<T>(lo[i], a & 0x000F000Fu, b & 0x000F000Fu, a8 & 0x000F000Fu,
-                           b8 & 0x000F000Fu, xr[0], xr[1], first);
-            mma_16x8x16<T>(hi[i], a & 0x00F000F0u, b & 0x00F000F0u, a8 & 0x00F000F0u,
-                           b8 & 0x00F000F0u, xr[2], xr[3], first);
-          } else {
-            constexpr uint32_t k128 = 0x43004300u;
-            mma_16x8x16<T>(lo[i], (a & 0x000F000Fu) | k128, (b & 0x000F000Fu) | k128,
-                           (a >> 4 & 0x000F000Fu) | k128, (b >> 4 & 0x000F000Fu) | k128, xr[0],
-                           xr[1], first);
-            mma_16x8x16<T>(lo[i], (a >> 8 & 0x000F000Fu) | k128, (b >> 8 & 0x000F000Fu) | k128,
-                           (a >> 12 & 0x000F000Fu) | k128, (b >> 12 & 0x000F000Fu) | k128, xr[2],
-                           xr[3], false);
-          }
+        for (int i = 0; i < U; ++i) {
+          mma_u8s8(lo[i], wa[i][w] & kLow, wb[i][w] & kLow, wa[i][w + 1] & kLow, wb[i][w + 1] & kLow,
+                   xr[0], xr[1], w == 0, 0);
+          mma_u8s8(hi[i], wa[i][w] & kHigh, wb[i][w] & kHigh, wa[i][w + 1] & kHigh,
+                   wb[i][w + 1] & kHigh, xr[2], xr[3], w == 0, kMagicBits);
         }
-        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[0], xr[1], first);
-        mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[2], xr[3], false);
+        mma_u8s8(sum, kOnes, kOnes, kOnes, kOnes, xr[0], xr[1], w == 0, kMagicBits);
+        mma_u8s8(sum, kOnes, kOnes, kOnes, kOnes, xr[2], xr[3], false, 0);
       }
     }
-    // the block's scales: rows g and g + 8 of each unit
+    // The block's scales: rows of number src and src + 8 of each unit.  16 times the sums of up to
+    // 128 columns stay below 2^22, and the float32 steps before the scale are exact.
+    const float S[2] = {__int_as_float(sum[0]) - kMagic, __int_as_float(sum[1]) - kMagic};
 #pragma unroll
-    for (int r = 0; r < (TWO ? 4 : 2); ++r) {
+    for (int r = 0; r < 2 * U; ++r) {
       const uint32_t sw = __shfl_sync(~0u, rg.s[j / 2], src + 8 * r);
       const float s = scale_value<T>(sw, j & 1);
       float z = kInt4Zero;
       if (ZP)
-        z = static_cast<float>(__shfl_sync(~0u, rg.z[j / 4], src + 8 * r) >> (8 * (j & 3)) & 0xFFu);
+        z = small_float(__shfl_sync(~0u, rg.z[j / 4], src + 8 * r) >> (8 * (j & 3)) & 0xFFu);
+      if (SUB > 1) z *= 16.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = r / 2, d = 2 * (r & 1) + h;
+        const int v = SUB > 1 ? lo[i][d] * 16 + hi[i][d] : hi[i][d];
+        acc[i][d] = fmaf(s, fmaf(-z, S[h], __int_as_float(v) - kMagic), acc[i][d]);
+      }
+    }
+  }
+}
+
+// The same with 16-bit operands; x: the lane's token's activations at the chunk's start.
+template <typename T, int SUB, bool ZP, bool TWO>
+__device__ __forceinline__ void add_chunk_16(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t row,
+                                          uint32_t swz, uint32_t x, int t, int src) {
+  constexpr int U = TWO ? 2 : 1;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr uint32_t kOne = kHalf ? 0x00100010u : 0x3F803F80u;  // 2^-20 or 1, twice
+  const uint32_t x_t = x + 16u * SUB * t;
+#pragma unroll
+  for (int j = 0; j < 8 / SUB; ++j) {
+    float lo[2][4], hi[2][4], sum[4];
+    const uint32_t at = row + ((16u * SUB * j + 4u * SUB * t) ^ swz);
+    uint32_t wa[2][SUB], wb[2][SUB];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      lds<SUB>(wa[i], at + i * kUnitBytes);
+      lds<SUB>(wb[i], at + i * kUnitBytes + 1024);
+    }
+#pragma unroll
+    for (int w = 0; w < SUB; ++w) {
+      const bool first = w == 0;
+      uint32_t xr[4];
+      lds<4>(xr, x_t + 64u * SUB * j + 16u * w);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t a = wa[i][w], b = wb[i][w];
+        if constexpr (kHalf) {
+          // the activations' words lie in the order 0, 2, 1, 3
+          const uint32_t a8 = a >> 8, b8 = b >> 8;
+          mma_16x8x16<T>(lo[i], a & 0x000F000Fu, b & 0x000F000Fu, a8 & 0x000F000Fu,
+                         b8 & 0x000F000Fu, xr[0], xr[1], first);
+          mma_16x8x16<T>(hi[i], a & 0x00F000F0u, b & 0x00F000F0u, a8 & 0x00F000F0u,
+                         b8 & 0x00F000F0u, xr[2], xr[3], first);
+        } else {
+          constexpr uint32_t k128 = 0x43004300u;
+          mma_16x8x16<T>(lo[i], (a & 0x000F000Fu) | k128, (b & 0x000F000Fu) | k128,
+                         (a >> 4 & 0x000F000Fu) | k128, (b >> 4 & 0x000F000Fu) | k128, xr[0],
+                         xr[1], first);
+          mma_16x8x16<T>(lo[i], (a >> 8 & 0x000F000Fu) | k128, (b >> 8 & 0x000F000Fu) | k128,
+                         (a >> 12 & 0x000F000Fu) | k128, (b >> 12 & 0x000F000Fu) | k128, xr[2],
+                         xr[3], false);
+        }
+      }
+      mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[0], xr[1], first);
+      mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[2], xr[3], false);
+    }
+    // the block's scales: rows g and g + 8 of each unit
+#pragma unroll
+    for (int r = 0; r < 2 * U; ++r) {
+      const uint32_t sw = __shfl_sync(~0u, rg.s[j / 2], src + 8 * r);
+      const float s = scale_value<T>(sw, j & 1);
+      float z = kInt4Zero;
+      if (ZP)
+        z = small_float(__shfl_sync(~0u, rg.z[j / 4], src + 8 * r) >> (8 * (j & 3)) & 0xFFu);
       if (!kHalf) z += 128.0f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -229,18 +321,41 @@ __device__ __forceinline__ void add_chunk(float (&acc)[2][4], const RowGroups<SU
   }
 }
 
+// e of the digits, from the float bits of the largest magnitude: that becomes 2^21 .. 1.97 * 2^21 (or
+// a little less), so that 0x8080 may be added below 2^22.  -148 .. 107.
+__device__ __forceinline__ int digit_exponent(uint32_t most) {
+  return static_cast<int>((most + 0x40000u) >> 23) - 127 - 21;
+}
+
+// The digits of 4 activations, scaled by f1 f2 to below 2^22 in magnitude: one word for each digit.
+// Rounded into the mantissa of kMagic, to nearest; with 0x8080 added, the number's low bytes are
+// d0 + 128 and d1 + 128, and the third is d2 + 64.
+__device__ __forceinline__ void digits4(const float (&f)[4], float f1, float f2, uint32_t (&d)[3]) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(fmaf(f[i] * f1, f2, kMagic + 32896.0f));
+  const uint32_t a = __byte_perm(v[0], v[1], 0x5140), b = __byte_perm(v[2], v[3], 0x5140);
+  d[0] = __byte_perm(a, b, 0x5410) ^ 0x80808080u;
+  d[1] = __byte_perm(a, b, 0x7632) ^ 0x80808080u;
+  const uint32_t c = __byte_perm(__byte_perm(v[0], v[1], 0x0062), __byte_perm(v[2], v[3], 0x0062), 0x5410);
+  d[2] = ((c | 0x80808080u) - 0x40404040u) ^ 0x80808080u;  // c - 64, byte by byte
+}
+
 }  // namespace
 
-template <typename T, int SUB, bool ZP>
+template <typename T, int SUB, bool ZP, bool DIGITS>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     int4_stream_kernel(const __grid_constant__ CUtensorMap map_w, const StreamArgs p) {
   extern __shared__ uint8_t stream_smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(stream_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warps = blockDim.x / 32;
+  const int cols = DIGITS ? 3 * p.M : p.M;  // of the activations' operand: digit d of token m is 3 m + d
+  const int part_floats = 32 * cols;        // a warp's partial sums of a pair
   uint8_t* xs = ring + static_cast<size_t>(warps) * p.stages * kStageBytes;
-  float* part = reinterpret_cast<float*>(xs + static_cast<size_t>(p.M) * p.xstride);
-  StreamShared& S = *reinterpret_cast<StreamShared*>(part + 2 * warps * 32 * p.M);
+  StreamShared& S = *reinterpret_cast<StreamShared*>(xs + static_cast<size_t>(cols) * p.xstride);
+  float* xscale = reinterpret_cast<float*>(&S + 1);  // DIGITS: 2^e, [token][chunk]
+  float* part = xscale + (DIGITS ? p.M * p.chunks : 0);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   volatile int* abort = &S.abort;
@@ -250,9 +365,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       for (int s = 0; s < p.stages; ++s) mbar_init(&S.full[w][s], 1);
     mbar_init(&S.x_full, 1);
     S.abort = 0;
-    fence_mbarrier_init();
     prefetch_tmap(&map_w);
   }
+  for (int i = threadIdx.x; i < p.chunks; i += blockDim.x) mbar_init(&S.x_ready[i], 1);
+  fence_mbarrier_init();
   __syncthreads();
   grid_launch_dependents();
 
@@ -294,40 +410,36 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   if (q < pairs) load_groups<SUB, ZP>(nxt, p, (u0 + 2 * q) * kUnitRows + lane, c * kChunkK);
 
   grid_dependency_wait();
-  if (threadIdx.x == 0) {
-    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2;
-    mbar_arrive_expect_tx(&S.x_full, row_bytes * p.M);
+  const int pieces = p.K / 8;  // 16 bytes, 8 columns; a lane takes one of each chunk and token
+  uint4 xv[2];                 // DIGITS: of the next chunk of the first pair
+  auto load_x = [&](int chunk) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int i = chunk * 32 + lane;
+      xv[m] = (m < p.M && i < pieces)
+                  ? reinterpret_cast<const uint4*>(static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K)[i]
+                  : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if constexpr (DIGITS) {
+    if (q == 0) load_x(c);
+  } else if (threadIdx.x == 0) {
+    const uint32_t bytes = static_cast<uint32_t>(p.K) * 2;
+    mbar_arrive_expect_tx(&S.x_full, bytes * p.M);
     for (int m = 0; m < p.M; ++m)
       bulk_load(xs + static_cast<size_t>(m) * p.xstride,
-                static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K, row_bytes, &S.x_full);
+                static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K, bytes, &S.x_full);
   }
-  // zeros behind the rows, up to the end of the last chunk
-  const int pad = p.chunks * kChunkK / 8 - p.K / 8;  // 16-byte pieces
-  for (int i = threadIdx.x; i < pad * p.M; i += blockDim.x)
-    *reinterpret_cast<uint4*>(xs + static_cast<size_t>(i / pad) * p.xstride + 2 * p.K + i % pad * 16) =
-        make_uint4(0, 0, 0, 0);
-  bool ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
-  if constexpr (std::is_same<T, __half>::value) {
-    // The two operand words of an MMA are a register pair: the words 0 and 2 of 16 bytes (the low
-    // nibbles' columns), then 1 and 3.
-    for (int m = 0; m < p.M; ++m) {
-      for (int i = threadIdx.x; i < p.K / 8; i += blockDim.x) {
-        uint32_t* v = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(m) * p.xstride) + 4 * i;
-        const uint32_t one = v[1], two = v[2];
-        v[1] = two;
-        v[2] = one;
-      }
-    }
-  }
-  __syncthreads();
 
   // Row g of an MMA is row `gr` of the unit, the bits of g reversed: the rows that read shared
   // memory together then differ in the swizzle's high bits (conflict-free for 4, 8 and 16 bytes).
   const int gr = (g & 1) << 2 | (g & 2) | g >> 2;
-  // columns past the last token repeat it: their results are not kept
-  const uint32_t x_lane = smem_addr(xs) + static_cast<uint32_t>(min(g, p.M - 1)) * p.xstride;
+  // columns past the last repeat it: their results are not kept
+  const uint32_t x_lane = smem_addr(xs) + static_cast<uint32_t>(min(g, cols - 1)) * p.xstride;
   const uint32_t w_lane = smem_addr(my_ring) + static_cast<uint32_t>(gr) * 128;
-  int stage = 0;
+  constexpr uint32_t kXChunk = kChunkK * (DIGITS ? 1 : 2);
+  bool ok = true;
+  int stage = 0, done = 0;  // pairs before `done` are stored
   uint32_t phase = 0;
   for (int pair = 0; pair < pairs; ++pair) {
     float acc[2][4] = {};
@@ -336,14 +448,89 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       int nq = q, nc = c + warps;
       settle(nq, nc);
       if (nq < pairs) load_groups<SUB, ZP>(nxt, p, (u0 + 2 * nq) * kUnitRows + lane, nc * kChunkK);
+      if (pair == 0) {
+        // this chunk's activations, for every pair
+        if constexpr (DIGITS) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (m < p.M) {
+              const uint4 v = xv[m];
+              // magnitudes of a 16-bit type compare as whole numbers
+              const uint32_t two = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                            __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+              const uint32_t most = __float_as_uint(
+                  unpack2<T>(__reduce_max_sync(~0u, max(two & 0xFFFFu, two >> 16))).x);
+              const int e = -digit_exponent(most);
+              const float f1 = __int_as_float((127 + e / 2) << 23);
+              const float f2 = __int_as_float((127 + e - e / 2) << 23);
+              const float2 p01 = unpack2<T>(v.x), p23 = unpack2<T>(v.y), p45 = unpack2<T>(v.z),
+                           p67 = unpack2<T>(v.w);
+              // bytes of a word's low nibbles: columns 0, 4, 1, 5; of its high ones: 2, 6, 3, 7
+              const float low[4] = {p01.x, p45.x, p01.y, p45.y};
+              const float high[4] = {p23.x, p67.x, p23.y, p67.y};
+              uint32_t dl[3], dh[3];
+              digits4(low, f1, f2, dl);
+              digits4(high, f1, f2, dh);
+              // one word: its low nibbles' digits, then its high ones'; two words: both low, then
+              // both high
+              const int i = c * 32 + lane, at = SUB == 1 ? 2 * i : (i & ~1) * 2 + (i & 1);
+#pragma unroll
+              for (int d = 0; d < 3; ++d) {
+                uint32_t* out =
+                    reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(3 * m + d) * p.xstride);
+                out[at] = dl[d];
+                out[at + (SUB == 1 ? 1 : 2)] = dh[d];
+              }
+              // 16 lo + hi is 16 times the sum
+              if (lane == 0)
+                xscale[m * p.chunks + c] = most >= 0x7F800000u ? __int_as_float(0x7FC00000)
+                                                               : ldexpf(SUB > 1 ? 0.0625f : 1.0f, -e);
+            }
+          }
+          if (nq == 0) load_x(nc);
+        } else {
+          if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
+          const int i = c * 32 + lane;
+          for (int m = 0; m < p.M; ++m) {
+            uint32_t* v = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(m) * p.xstride) + 4 * i;
+            if (i >= pieces) {  // zeros up to the chunk's end
+              *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
+            } else if (std::is_same<T, __half>::value) {
+              // The two operand words of an MMA are a register pair: the words 0 and 2 of 16 bytes
+              // (the low nibbles' columns), then 1 and 3.
+              const uint32_t one = v[1], two = v[2];
+              v[1] = two;
+              v[2] = one;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.x_ready[c]);
+      } else if (ok) {
+        ok = __all_sync(~0u, mbar_wait_bounded(&S.x_ready[c], 0, abort));
+      }
       if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&my_full[stage], phase, abort));
       if (ok) {
         const uint32_t w = w_lane + static_cast<uint32_t>(stage) * kStageBytes;
-        const uint32_t x = x_lane + 2u * kChunkK * c;
-        if (u0 + 2 * pair + 1 < u1)
-          add_chunk<T, SUB, ZP, true>(acc, cur, w, 16u * gr, x, t, gr);
-        else
-          add_chunk<T, SUB, ZP, false>(acc, cur, w, 16u * gr, x, t, gr);
+        const uint32_t x = x_lane + kXChunk * c;
+        const bool two = u0 + 2 * pair + 1 < u1;
+        if constexpr (DIGITS) {
+          float chunk[2][4] = {};
+          if (two) add_chunk_digits<T, SUB, ZP, true>(chunk, cur, w, 16u * gr, x, t, gr);
+          else add_chunk_digits<T, SUB, ZP, false>(chunk, cur, w, 16u * gr, x, t, gr);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = xscale[min((2 * t + h) / 3, p.M - 1) * p.chunks + c];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int d = 2 * (r & 1) + h;
+              acc[r / 2][d] = fmaf(f, chunk[r / 2][d], acc[r / 2][d]);
+            }
+          }
+        } else {
+          if (two) add_chunk_16<T, SUB, ZP, true>(acc, cur, w, 16u * gr, x, t, gr);
+          else add_chunk_16<T, SUB, ZP, false>(acc, cur, w, 16u * gr, x, t, gr);
+        }
       }
       __syncwarp();
       if (ok) request();
@@ -351,29 +538,44 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       q = nq;
       c = nc;
     }
-    // the pair's partial sums: [token][row] of each warp
-    float* mine = part + ((pair & 1) * warps + warp) * 32 * p.M;
+    // the pair's partial sums, [column][row] of each warp, in the last 2 batch pairs' places
+    float* mine = part + (pair % (2 * p.batch) * warps + warp) * part_floats;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int m = 2 * t + h;
-      if (m < p.M) {
+      if (m < cols) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) mine[m * 32 + gr + 8 * r] = acc[r / 2][2 * (r & 1) + h];
       }
     }
+    if ((pair + 1) % p.batch != 0 && pair + 1 < pairs) continue;
     __syncthreads();
-    const int row0 = (u0 + 2 * pair) * kUnitRows;
-    const int row_end = min(p.N, u1 * kUnitRows);
-    const float* all = part + (pair & 1) * warps * 32 * p.M;
-    for (int i = threadIdx.x; i < 32 * p.M; i += blockDim.x) {
-      const int n = row0 + (i & 31), m = i >> 5;
-      if (n >= row_end) continue;
-      float v = 0.0f;
-      for (int w = 0; w < warps; ++w) v += all[w * 32 * p.M + i];
-      if (std::is_same<T, __half>::value) v *= 1048576.0f;  // the sums are of 2^-20 u X
-      if (p.bias) v += to_f32(static_cast<const T*>(p.bias)[n]);
-      static_cast<T*>(p.Y)[static_cast<size_t>(m) * p.N + n] = from_f32<T>(v);
+    // a warp adds up 32 rows of one token: the first warps after the batch's last pair's number
+    for (int o = (warp + pair) % warps; o < (pair + 1 - done) * p.M; o += warps) {
+      const int from = done + o / p.M, m = o % p.M;
+      const float* sums = part + from % (2 * p.batch) * warps * part_floats + lane;
+      float v;
+      if constexpr (DIGITS) {
+        float d[3] = {};
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) {
+#pragma unroll
+          for (int e = 0; e < 3; ++e) d[e] += sums[w * part_floats + (3 * m + e) * 32];
+        }
+        v = fmaf(d[2], 65536.0f, fmaf(d[1], 256.0f, d[0]));
+      } else {
+        v = 0.0f;
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) v += sums[w * part_floats + m * 32];
+        if (std::is_same<T, __half>::value) v *= 1048576.0f;  // the sums are of 2^-20 u X
+      }
+      const int n = (u0 + 2 * from) * kUnitRows + lane;
+      if (n < min(p.N, u1 * kUnitRows)) {
+        if (p.bias) v += to_f32(static_cast<const T*>(p.bias)[n]);
+        static_cast<T*>(p.Y)[static_cast<size_t>(m) * p.N + n] = from_f32<T>(v);
+      }
     }
+    done = pair + 1;
   }
   if (!ok) {
     if (lane == 0 && p.status)
@@ -382,41 +584,56 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     int dummy = 0;
     for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; ++j)
       mbar_wait_bounded(&my_full[j % p.stages], static_cast<uint32_t>(j / p.stages) & 1u, &dummy);
+    if (!DIGITS) mbar_wait_bounded(&S.x_full, 0, &dummy);
   }
 }
 
 namespace {
 
 struct StreamPlan {
-  int warps, stages, xstride;
+  int warps, per_sm, stages, xstride, batch;
   size_t smem;
 };
 
-// Fits where the activations of all tokens leave room for two stages of 8 warps.
+// Columns of 32 SUB are one load of a lane and lie in one group.
+int sub_of(int group) { return group == 32 ? 1 : group == 64 ? 2 : 4; }
+
+// Two blocks of 8 warps on an SM where the activations of all tokens leave room for that, otherwise
+// one of 16 or 8; at least two stages for each warp.  (One token, fp16, groups of 128, us of two
+// blocks of 8 / one of 16 / one of 8: 2368 x 4096 4.0 / 5.5 / 5.1, 16384 x 4096 10.1 / 17.1 / 12.6,
+// 49152 x 12288 57 / 55 / 73; two tokens of 32768 x 8192, where two blocks do not fit, - / 33 / 37.)
 bool plan_stream(int M, int K, int group, StreamPlan& s) {
   if (M > kMaxTok) return false;
-  // a row up to its last chunk's end, and a pad that sets the quads of two tokens apart (64 bytes
-  // where a lane reads every fourth 16 bytes, otherwise 16)
-  s.xstride = (K + kChunkK - 1) / kChunkK * kChunkK * 2 + (group == 32 ? 64 : 16);
-  for (int warps = kMaxWarps; warps >= 8; warps /= 2) {
-    const size_t fixed = 1024 + sizeof(StreamShared) + static_cast<size_t>(M) * s.xstride +
-                         static_cast<size_t>(2) * warps * 32 * M * sizeof(float);
-    for (int stages = kMaxStages; stages >= 2; --stages) {
-      s.smem = fixed + static_cast<size_t>(warps) * stages * kStageBytes;
-      if (s.smem <= kSmemMost) {
-        s.warps = warps;
-        s.stages = stages;
-        return true;
+  const bool digits = M <= 2;
+  const int sub = sub_of(group), cols = digits ? 3 * M : M;
+  const int chunks = (K + kChunkK - 1) / kChunkK;
+  // a column's activations up to the last chunk's end, and a pad that sets the quads of two columns
+  // apart: 8, 16 or 32 bytes a lane of digits, twice that in 16 bits
+  s.xstride = chunks * kChunkK * (digits ? 1 : 2) +
+              (digits ? (sub == 1 ? 32 : sub == 2 ? 64 : 16) : (sub == 1 ? 64 : 16));
+  const struct { int warps, per_sm; } shapes[] = {{8, 2}, {16, 1}, {8, 1}};
+  for (const auto& shape : shapes) {
+    s.warps = shape.warps;
+    s.per_sm = shape.per_sm;
+    const size_t most = shape.per_sm == 2 ? kSmemMost / 2 : kSmemMost;
+    const size_t pair_bytes = static_cast<size_t>(s.warps) * 32 * cols * sizeof(float);
+    const size_t fixed = 1024 + static_cast<size_t>(cols) * s.xstride + sizeof(StreamShared) +
+                         (digits ? M * chunks * sizeof(float) : 0);
+    for (s.stages = kMaxStages; s.stages >= 2; --s.stages) {
+      const size_t ring = static_cast<size_t>(s.warps) * s.stages * kStageBytes;
+      for (s.batch = 4; s.batch >= 1; s.batch /= 2) {
+        s.smem = fixed + ring + 2 * s.batch * pair_bytes;
+        if (s.smem <= most) return true;
       }
     }
   }
   return false;
 }
 
-template <typename T, int SUB, bool ZP>
+template <typename T, int SUB, bool ZP, bool DIGITS>
 cudaError_t launch_variant(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s,
                            int grid, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(int4_stream_kernel<T, SUB, ZP>,
+  cudaError_t e = cudaFuncSetAttribute(int4_stream_kernel<T, SUB, ZP, DIGITS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemMost));
   if (e != cudaSuccess) return e;
@@ -430,16 +647,27 @@ cudaError_t launch_variant(const CUtensorMap& map, const StreamArgs& p, const St
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, int4_stream_kernel<T, SUB, ZP>, map, p);
+  return cudaLaunchKernelEx(&cfg, int4_stream_kernel<T, SUB, ZP, DIGITS>, map, p);
 }
 
-template <typename T, bool ZP>
-cudaError_t launch_sub(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s, int grid,
-                       cudaStream_t stream) {
-  if (p.group == 32) return launch_variant<T, 1, ZP>(map, p, s, grid, stream);
-  if (p.group == 64) return launch_variant<T, 2, ZP>(map, p, s, grid, stream);
-  if (p.group % 256 == 0) return launch_variant<T, 8, ZP>(map, p, s, grid, stream);
-  return launch_variant<T, 4, ZP>(map, p, s, grid, stream);
+template <typename T, bool ZP, bool DIGITS>
+cudaError_t launch_sub(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s,
+                       int grid, cudaStream_t stream) {
+  switch (sub_of(p.group)) {
+    case 1: return launch_variant<T, 1, ZP, DIGITS>(map, p, s, grid, stream);
+    case 2: return launch_variant<T, 2, ZP, DIGITS>(map, p, s, grid, stream);
+    default: return launch_variant<T, 4, ZP, DIGITS>(map, p, s, grid, stream);
+  }
+}
+
+template <typename T>
+cudaError_t launch_typed(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s,
+                         int grid, cudaStream_t stream) {
+  if (p.M <= 2)
+    return p.zeros ? launch_sub<T, true, true>(map, p, s, grid, stream)
+                   : launch_sub<T, false, true>(map, p, s, grid, stream);
+  return p.zeros ? launch_sub<T, true, false>(map, p, s, grid, stream)
+                 : launch_sub<T, false, false>(map, p, s, grid, stream);
 }
 
 }  // namespace
@@ -473,14 +701,12 @@ cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_
   p.chunks = (w.K + kChunkK - 1) / kChunkK;
   p.stages = s.stages;
   p.xstride = s.xstride;
+  p.batch = s.batch;
+  const int grid = p.units < num_sms * s.per_sm ? p.units : num_sms * s.per_sm;
   const int blocks = w.group == 32 ? 8 : w.group == 64 ? 4 : 2;  // groups in a chunk
   p.vector_groups = w.group <= 128 && w.groups % blocks == 0;
-  const int grid = p.units < num_sms ? p.units : num_sms;
-  if (w.bf16)
-    return w.zeros ? launch_sub<__nv_bfloat16, true>(map, p, s, grid, stream)
-                   : launch_sub<__nv_bfloat16, false>(map, p, s, grid, stream);
-  return w.zeros ? launch_sub<__half, true>(map, p, s, grid, stream)
-                 : launch_sub<__half, false>(map, p, s, grid, stream);
+  return w.bf16 ? launch_typed<__nv_bfloat16>(map, p, s, grid, stream)
+                : launch_typed<__half>(map, p, s, grid, stream);
 }
 
 }  // namespace i8mm
