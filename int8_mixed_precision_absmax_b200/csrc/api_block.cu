@@ -164,7 +164,7 @@ int int8_block_residual(const void* f, const void* x, int M, int D, const void* 
   a.h = h;
   a.M = M;
   a.D = D;
-  a.gate_rows = gate_rows;
+  a.rows_per_gate = gate ? M / gate_rows : 1;
   a.x_scale = x_scale;
   a.f_scale = f_scale;
   a.eps = eps;

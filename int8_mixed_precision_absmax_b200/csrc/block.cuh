@@ -113,7 +113,7 @@ struct BlockNormArgs {
   void* y;                  // R [M, D] or null
   void* h;                  // T [M, D] or null
   int M, D;
-  int gate_rows;            // 0 without a gate
+  int rows_per_gate;        // rows that share a gate row
   float x_scale, f_scale, eps;
   bool bf16, layer_norm, f32_residual, post_norm;
 };
