@@ -75,6 +75,51 @@ __host__ __device__ constexpr int int4_nibble(int j) { return (j & 1) * 4 + (j >
 
 constexpr int kInt4Zero = 8;  // the zero point where none is given
 
+// W_hat of 4-bit words: the group's constants, and 8 values of a word.  A nibble set into the low
+// mantissa bits of 1024 (fp16) or 128 (bf16) reads as that number plus the code.
+template <typename T>
+struct Int4Values;
+template <>
+struct Int4Values<__half> {
+  __half2 s, z0, z1;
+  __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
+    s = *reinterpret_cast<const __half2*>(&s2);
+    const float zf = static_cast<float>(z);
+    z0 = __float2half2_rn(1024.0f + zf);   // exact up to 2048
+    z1 = __float2half2_rn(-64.0f - zf);    // of a code in bits 4..7: (1024 + 16 u) / 16
+  }
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    const uint32_t w8 = w >> 8;
+    const uint32_t a[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u,
+                           (w8 & 0x000F000Fu) | 0x64006400u, (w8 & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&a[i]);
+      const __half2 d = (i & 1) ? __hfma2(h, sixteenth, z1) : __hsub2(h, z0);
+      const __half2 v = __hmul2(d, s);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+template <>
+struct Int4Values<__nv_bfloat16> {
+  __nv_bfloat162 s, z0;
+  __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
+    s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+    z0 = __float2bfloat162_rn(128.0f + static_cast<float>(z));
+  }
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      const __nv_bfloat162 v =
+          __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), z0), s);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+
 struct Int4Weight {
   const uint8_t* codes;
   const void* scales;    // T [N, groups]

@@ -1,5 +1,12 @@
 // int4.cu -- 4-bit weights with group scales: the quantizer, its inverse, and which kernel multiplies.
+//
+// Both passes are bound by the bytes of the 16-bit weights (one read or one write, and a quarter of
+// that for the codes).  A lane takes 16 neighbouring columns at a time, so a group's scale is found
+// once for 16 values, and asks for its next ones before it works on those it has.
+#include <type_traits>
+
 #include "block.cuh"
+#include "codes.cuh"
 
 namespace i8mm {
 
@@ -8,37 +15,40 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// The maximum over the `width` lanes of a warp segment (a power of two up to 32).
-__device__ __forceinline__ float seg_max(float v, int width) {
-  for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
-}
-
-// The largest w and -w of 8 neighbours (at least 0), and whether any is NaN or infinite.
+// The extremes of values of type T, two at a time: the largest and the smallest, a NaN wherever one
+// of them is.
 template <typename T>
-__device__ __forceinline__ void extremes8(const uint4& v, float& hi, float& nlo, bool& bad) {
-  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack2<T>(r[i]);
-    hi = fmaxf(hi, fmaxf(p.x, p.y));
-    nlo = fmaxf(nlo, fmaxf(-p.x, -p.y));
-    bad |= !(fabsf(p.x) <= 3.4028235e38f) || !(fabsf(p.y) <= 3.4028235e38f);
+struct Extremes {
+  using T2 = typename Half2Of<T>::type;
+  T2 hi, lo;
+  static __device__ __forceinline__ T2 of(uint32_t w) { return *reinterpret_cast<T2*>(&w); }
+  __device__ __forceinline__ void start() {
+    const uint32_t zero = 0;
+    hi = lo = of(zero);
   }
-}
+  __device__ __forceinline__ void add(uint32_t w) {
+    hi = __hmax2_nan(hi, of(w));
+    lo = __hmin2_nan(lo, of(w));
+  }
+  // over the lanes of a segment of `width`
+  __device__ __forceinline__ void join(int width) {
+    for (int o = width / 2; o > 0; o >>= 1) {
+      hi = __hmax2_nan(hi, of(__shfl_xor_sync(~0u, *reinterpret_cast<uint32_t*>(&hi), o)));
+      lo = __hmin2_nan(lo, of(__shfl_xor_sync(~0u, *reinterpret_cast<uint32_t*>(&lo), o)));
+    }
+  }
+};
 
-// Scale and zero point of a group from its extremes (hi = max(w, 0), nlo = max(-w, 0)).
+// Scale and zero point of a group from its extremes (hi = max(w, 0), nlo = max(-w, 0), or a NaN).
 template <typename T>
-__device__ __forceinline__ void group_params(float hi, float nlo, bool bad, bool affine, T& s,
-                                             float& z) {
-  if (bad) {
+__device__ __forceinline__ void group_params(float hi, float nlo, bool affine, T& s, float& z) {
+  z = kInt4Zero;
+  if (!(hi <= 3.4028235e38f && nlo <= 3.4028235e38f)) {
     s = from_f32<T>(__int_as_float(0x7FC00000));
-    z = kInt4Zero;
     return;
   }
   if (!affine) {
     s = from_f32<T>(__fdiv_rn(fmaxf(hi, nlo), 7.0f));
-    z = kInt4Zero;
     return;
   }
   s = from_f32<T>(__fadd_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(nlo, 15.0f)));
@@ -46,86 +56,221 @@ __device__ __forceinline__ void group_params(float hi, float nlo, bool bad, bool
   z = sf > 0.0f ? fminf(rintf(__fdiv_rn(nlo, sf)), 15.0f) : 0.0f;
 }
 
+// Whether the quotients by s can be had from its reciprocal without leaving float32's normal range,
+// and s is rounded to T finely enough (half a step of 2^-8) that |w / s| stays below 7.5.
 template <typename T>
-__device__ __forceinline__ uint32_t encode8(const uint4& v, float s, float z, bool affine) {
+__device__ __forceinline__ bool plain_scale(float s) {
+  return std::is_same<T, __half>::value ? s >= 6.2e-5f : s >= 1e-30f && s <= 1e30f;
+}
+
+// The word of 8 neighbours, two at a time in the order of the word's halves.  w / s is w (1/s) put
+// right by its remainder (Markstein: the correctly rounded quotient, given the correctly rounded
+// reciprocal); adding 1.5 2^23 rounds it to a whole number, ties to even.  Four codes of a half are
+// one number below 2^16.
+template <typename T, bool AFFINE>
+__device__ __forceinline__ uint32_t encode8(const uint4& v, float s, float inv, float z) {
   const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-  const float lo = affine ? 0.0f : 1.0f;
+  const uint64_t s2 = f32x2_pack(-s, -s), inv2 = f32x2_pack(inv, inv), k16 = f32x2_pack(16.0f, 16.0f);
+  const uint64_t up = f32x2_pack(12582912.0f, 12582912.0f);
+  const uint64_t down = f32x2_pack(z - 12582912.0f, z - 12582912.0f);
+  uint64_t acc = 0;
+#pragma unroll
+  for (int j = 3; j >= 0; --j) {
+    const float2 f = unpack2<T>(r[j]);
+    const uint64_t w = f32x2_pack(f.x, f.y);
+    uint64_t q = f32x2_mul(w, inv2);
+    q = f32x2_fma(f32x2_fma(q, s2, w), inv2, q);
+    uint64_t u = f32x2_add(f32x2_add(q, up), down);
+    if (AFFINE) {  // both extremes may have been rounded away from the zero point
+      uint32_t x, y;
+      f32x2_unpack(u, x, y);
+      u = f32x2_pack(fminf(__uint_as_float(x), 15.0f), fminf(__uint_as_float(y), 15.0f));
+    }
+    acc = j == 3 ? u : f32x2_fma(acc, k16, u);
+  }
+  uint32_t even, odd;
+  f32x2_unpack(f32x2_add(acc, f32x2_pack(8388608.0f, 8388608.0f)), even, odd);
+  return __byte_perm(even, odd, 0x5410);
+}
+
+// The same by the definition, for any scale.
+template <typename T, bool AFFINE>
+__device__ __noinline__ uint32_t encode8_any(uint4 v, float s, float z) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
   uint32_t word = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float2 p = unpack2<T>(r[j / 2]);
     const float w = (j & 1) ? p.y : p.x;
     float u = z;
-    if (s > 0.0f) u = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(w, s)), z), lo), 15.0f);
+    if (s > 0.0f) u = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(w, s)), z), AFFINE ? 0.0f : 1.0f), 15.0f);
     word |= static_cast<uint32_t>(u) << (4 * int4_nibble(j));
   }
   return word;
 }
 
+// Goes through the spans of `n` rows in steps of all warps of the grid, without divisions.
+struct SpanWalk {
+  long long row;
+  int span, d_span;
+  long long d_row;
+  int spans;
+  __device__ __forceinline__ SpanWalk(int spans_) : spans(spans_) {
+    const long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+    const long long step = static_cast<long long>(gridDim.x) * kWarps;
+    row = i / spans;
+    span = static_cast<int>(i % spans);
+    d_row = step / spans;
+    d_span = static_cast<int>(step % spans);
+  }
+  __device__ __forceinline__ void next() {
+    row += d_row;
+    span += d_span;
+    if (span >= spans) {
+      span -= spans;
+      ++row;
+    }
+  }
+};
+
 }  // namespace
 
-// One warp per span of `span` columns of a row (256, or the whole group where a group is longer
-// or no power of two); a group of up to 256 columns is a segment of span lanes.
-template <typename T>
+// Groups of 32, 64, 128 or 256 columns: `width` lanes of 16 columns each; a warp takes 512 columns.
+template <typename T, bool AFFINE>
 __global__ void __launch_bounds__(kThreads)
-    int4_quant_kernel(const T* __restrict__ W, int N, int K, int group, int groups, int span,
+    int4_quant_kernel(const T* __restrict__ W, int N, int K, int width, int groups,
                       uint8_t* __restrict__ codes, T* __restrict__ scales,
                       uint8_t* __restrict__ zeros) {
   const int lane = threadIdx.x & 31;
-  const int spans = (K + span - 1) / span;
-  const long long total = static_cast<long long>(N) * spans;
-  const int width = group <= 256 ? group / 8 : 32;  // lanes of a group
-  const bool affine = zeros != nullptr;
-  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; i < total;
-       i += static_cast<long long>(gridDim.x) * kWarps) {
-    const long long n = i / spans;
-    const int k0 = static_cast<int>(i % spans) * span;
-    const int k1 = min(K, k0 + span);
-    const uint4* row = reinterpret_cast<const uint4*>(W + n * K);
-    float hi = 0.0f, nlo = 0.0f;
-    bool bad = false;
-    for (int k = k0 + lane * 8; k < k1; k += 256) extremes8<T>(row[k / 8], hi, nlo, bad);
-    hi = seg_max(hi, width);
-    nlo = seg_max(nlo, width);
-    bad = seg_max(bad ? 1.0f : 0.0f, width) > 0.0f;
+  const int group_shift = 4 + __ffs(width) - 1;
+  SpanWalk at((K + 511) / 512);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 v0 = none, v1 = none;
+  auto fetch = [&]() {
+    const int k = at.span * 512 + lane * 16;
+    v0 = v1 = none;
+    if (at.row < N && k < K) {
+      const uint4* p = reinterpret_cast<const uint4*>(W + at.row * K + k);
+      v0 = __ldcs(p);
+      v1 = __ldcs(p + 1);
+    }
+  };
+  fetch();
+  while (at.row < N) {
+    const uint4 a = v0, b = v1;
+    const long long row = at.row;
+    const int k = at.span * 512 + lane * 16;
+    at.next();
+    fetch();
+    Extremes<T> e;
+    e.start();
+    e.add(a.x), e.add(a.y), e.add(a.z), e.add(a.w);
+    e.add(b.x), e.add(b.y), e.add(b.z), e.add(b.w);
+    e.join(width);
+    const float hx = to_f32(e.hi.x), hy = to_f32(e.hi.y), lx = -to_f32(e.lo.x), ly = -to_f32(e.lo.y);
+    // (a NaN in either half: fmaxf would drop it)
+    const float hi = hx != hx ? hx : hy != hy ? hy : fmaxf(hx, hy);
+    const float nlo = lx != lx ? lx : ly != ly ? ly : fmaxf(lx, ly);
     T s;
     float z;
-    group_params<T>(hi, nlo, bad, affine, s, z);
+    group_params<T>(hi, nlo, AFFINE, s, z);
     const float sf = to_f32(s);
-    const int k = k0 + lane * 8;
-    if (k < k1 && lane % width == 0) {
-      scales[n * groups + k / group] = s;
-      if (affine) zeros[n * groups + k / group] = static_cast<uint8_t>(z);
+    uint32_t w0, w1;
+    if (plain_scale<T>(sf)) {
+      const float inv = __frcp_rn(sf);
+      w0 = encode8<T, AFFINE>(a, sf, inv, z);
+      w1 = encode8<T, AFFINE>(b, sf, inv, z);
+    } else {
+      w0 = encode8_any<T, AFFINE>(a, sf, z);
+      w1 = encode8_any<T, AFFINE>(b, sf, z);
     }
-    uint32_t* out = reinterpret_cast<uint32_t*>(codes + n * (K / 2));
-    for (int c = k; c < k1; c += 256) out[c / 8] = encode8<T>(row[c / 8], sf, z, affine);
+    if (k < K) {
+      __stcs(reinterpret_cast<uint2*>(codes + row * (K / 2) + k / 2), make_uint2(w0, w1));
+      if ((lane & (width - 1)) == 0) {
+        scales[row * groups + (k >> group_shift)] = s;
+        if (AFFINE) zeros[row * groups + (k >> group_shift)] = static_cast<uint8_t>(z);
+      }
+    }
   }
 }
 
-// One thread per word.
+// Other groups (multiples of 128, or a whole row): one warp per group, which it reads twice.
+template <typename T, bool AFFINE>
+__global__ void __launch_bounds__(kThreads)
+    int4_quant_long_kernel(const T* __restrict__ W, int N, int K, int group, int groups,
+                           uint8_t* __restrict__ codes, T* __restrict__ scales,
+                           uint8_t* __restrict__ zeros) {
+  const int lane = threadIdx.x & 31;
+  for (SpanWalk at(groups); at.row < N; at.next()) {
+    const int k0 = at.span * group, k1 = static_cast<int>(min(static_cast<long long>(K), static_cast<long long>(k0) + group));
+    const uint4* row = reinterpret_cast<const uint4*>(W + at.row * K);
+    Extremes<T> e;
+    e.start();
+    for (int k = k0 + lane * 8; k < k1; k += 256) {
+      const uint4 a = row[k / 8];
+      e.add(a.x), e.add(a.y), e.add(a.z), e.add(a.w);
+    }
+    e.join(32);
+    const float hx = to_f32(e.hi.x), hy = to_f32(e.hi.y), lx = -to_f32(e.lo.x), ly = -to_f32(e.lo.y);
+    const float hi = hx != hx ? hx : hy != hy ? hy : fmaxf(hx, hy);
+    const float nlo = lx != lx ? lx : ly != ly ? ly : fmaxf(lx, ly);
+    T s;
+    float z;
+    group_params<T>(hi, nlo, AFFINE, s, z);
+    const float sf = to_f32(s);
+    const bool plain = plain_scale<T>(sf);
+    const float inv = plain ? __frcp_rn(sf) : 0.0f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(codes + at.row * (K / 2));
+    for (int k = k0 + lane * 8; k < k1; k += 256)
+      out[k / 8] = plain ? encode8<T, AFFINE>(row[k / 8], sf, inv, z)
+                         : encode8_any<T, AFFINE>(row[k / 8], sf, z);
+    if (lane == 0) {
+      scales[at.row * groups + at.span] = s;
+      if (AFFINE) zeros[at.row * groups + at.span] = static_cast<uint8_t>(z);
+    }
+  }
+}
+
+// A warp takes 512 columns: each lane the words lane and lane + 32 of them.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     int4_dequant_kernel(const uint32_t* __restrict__ codes, const T* __restrict__ scales,
-                        const uint8_t* __restrict__ zeros, int N, int K, int group, int groups,
+                        const uint8_t* __restrict__ zeros, int N, int K, unsigned group, int groups,
                         uint4* __restrict__ W_hat) {
+  const int lane = threadIdx.x & 31;
   const int words = K / 8;
-  const long long total = static_cast<long long>(N) * words;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long n = i / words;
-    const int k = static_cast<int>(i % words) * 8;
-    const long long c = n * groups + k / group;
-    const float s = to_f32(scales[c]);
-    const float z = zeros ? static_cast<float>(zeros[c]) : static_cast<float>(kInt4Zero);
-    const uint32_t w = codes[i];
-    uint32_t r[4];
+  SpanWalk at((K + 511) / 512);
+  const uint16_t* s16 = reinterpret_cast<const uint16_t*>(scales);
+  uint32_t word[2], scale[2], zero[2];
+  auto fetch = [&]() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = static_cast<float>((w >> (4 * j)) & 15u) - z;
-      const float b = static_cast<float>((w >> (4 * j + 16)) & 15u) - z;
-      r[j] = pack2<T>(a * s, b * s);
+    for (int i = 0; i < 2; ++i) {
+      const int j = at.span * 64 + i * 32 + lane;
+      if (at.row < N && j < words) {
+        const long long c = at.row * groups + static_cast<unsigned>(j * 8) / group;
+        word[i] = __ldcs(codes + at.row * words + j);
+        scale[i] = s16[c];
+        zero[i] = zeros ? zeros[c] : kInt4Zero;
+      }
     }
-    W_hat[i] = make_uint4(r[0], r[1], r[2], r[3]);
+  };
+  fetch();
+  while (at.row < N) {
+    const uint32_t w[2] = {word[0], word[1]}, s[2] = {scale[0], scale[1]}, z[2] = {zero[0], zero[1]};
+    const long long row = at.row;
+    const int j0 = at.span * 64 + lane;
+    at.next();
+    fetch();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (j0 + i * 32 < words) {
+        Int4Values<T> q;
+        uint32_t r[4];
+        q.set(s[i] * 0x10001u, z[i]);
+        q.word(w[i], r);
+        __stcs(W_hat + row * words + j0 + i * 32, make_uint4(r[0], r[1], r[2], r[3]));
+      }
+    }
   }
 }
 
@@ -137,34 +282,41 @@ int blocks_for(long long work, int per_block, int num_sms) {
   return static_cast<int>(want < most ? want : most);
 }
 
+template <typename T, bool AFFINE>
+cudaError_t quant_typed(const void* W, int N, int K, int group, uint8_t* codes, void* scales,
+                        uint8_t* zeros, int num_sms, cudaStream_t stream) {
+  const int groups = int4_groups(K, group);
+  const bool short_groups = group == 32 || group == 64 || group == 128 || group == 256;
+  const long long spans = short_groups ? (K + 511) / 512 : groups;
+  const int grid = blocks_for(spans * N, kWarps, num_sms);
+  if (short_groups)
+    int4_quant_kernel<T, AFFINE><<<grid, kThreads, 0, stream>>>(
+        static_cast<const T*>(W), N, K, group / 16, groups, codes, static_cast<T*>(scales), zeros);
+  else
+    int4_quant_long_kernel<T, AFFINE><<<grid, kThreads, 0, stream>>>(
+        static_cast<const T*>(W), N, K, group, groups, codes, static_cast<T*>(scales), zeros);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_int4_quant(const void* W, int N, int K, int group, bool bf16, uint8_t* codes,
                               void* scales, uint8_t* zeros, int num_sms, cudaStream_t stream) {
-  const int groups = int4_groups(K, group);
-  const int span = (group == 32 || group == 64 || group == 128 || group == 256) ? 256 : group;
-  const long long total = static_cast<long long>(N) * ((K + span - 1) / span);
-  const int grid = blocks_for(total, kWarps, num_sms);
   if (bf16)
-    int4_quant_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(W), N, K, group, groups, span, codes,
-        static_cast<__nv_bfloat16*>(scales), zeros);
-  else
-    int4_quant_kernel<__half><<<grid, kThreads, 0, stream>>>(static_cast<const __half*>(W), N, K,
-                                                             group, groups, span, codes,
-                                                             static_cast<__half*>(scales), zeros);
-  return cudaGetLastError();
+    return zeros ? quant_typed<__nv_bfloat16, true>(W, N, K, group, codes, scales, zeros, num_sms, stream)
+                 : quant_typed<__nv_bfloat16, false>(W, N, K, group, codes, scales, zeros, num_sms, stream);
+  return zeros ? quant_typed<__half, true>(W, N, K, group, codes, scales, zeros, num_sms, stream)
+               : quant_typed<__half, false>(W, N, K, group, codes, scales, zeros, num_sms, stream);
 }
 
 cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
                                 cudaStream_t stream) {
-  const int grid = blocks_for(static_cast<long long>(w.N) * (w.K / 8), kThreads, num_sms);
+  const int grid = blocks_for(static_cast<long long>(w.N) * ((w.K + 511) / 512), kWarps, num_sms);
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(w.codes);
   uint4* out = static_cast<uint4*>(W_hat);
   if (w.bf16)
     int4_dequant_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(
-        codes, static_cast<const __nv_bfloat16*>(w.scales), w.zeros, w.N, w.K, w.group, w.groups,
-        out);
+        codes, static_cast<const __nv_bfloat16*>(w.scales), w.zeros, w.N, w.K, w.group, w.groups, out);
   else
     int4_dequant_kernel<__half><<<grid, kThreads, 0, stream>>>(
         codes, static_cast<const __half*>(w.scales), w.zeros, w.N, w.K, w.group, w.groups, out);
