@@ -15,72 +15,95 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// The extremes of values of type T, two at a time: the largest and the smallest, a NaN wherever one
-// of them is.
-template <typename T>
+// The extremes of values of type T, two at a time: the largest and, where AFFINE, the smallest, or
+// else the largest magnitude; a NaN wherever one of the values is.
+template <typename T, bool AFFINE>
 struct Extremes {
   using T2 = typename Half2Of<T>::type;
   T2 hi, lo;
   static __device__ __forceinline__ T2 of(uint32_t w) { return *reinterpret_cast<T2*>(&w); }
-  __device__ __forceinline__ void start() {
-    const uint32_t zero = 0;
-    hi = lo = of(zero);
+  static __device__ __forceinline__ T2 from(T2 v, int o) {
+    return of(__shfl_xor_sync(~0u, *reinterpret_cast<uint32_t*>(&v), o));
   }
+  __device__ __forceinline__ void start() { hi = lo = of(0u); }
   __device__ __forceinline__ void add(uint32_t w) {
-    hi = __hmax2_nan(hi, of(w));
-    lo = __hmin2_nan(lo, of(w));
+    hi = __hmax2_nan(hi, AFFINE ? of(w) : __habs2(of(w)));
+    if (AFFINE) lo = __hmin2_nan(lo, of(w));
   }
   // over the lanes of a segment of `width`
   __device__ __forceinline__ void join(int width) {
     for (int o = width / 2; o > 0; o >>= 1) {
-      hi = __hmax2_nan(hi, of(__shfl_xor_sync(~0u, *reinterpret_cast<uint32_t*>(&hi), o)));
-      lo = __hmin2_nan(lo, of(__shfl_xor_sync(~0u, *reinterpret_cast<uint32_t*>(&lo), o)));
+      hi = __hmax2_nan(hi, from(hi, o));
+      if (AFFINE) lo = __hmin2_nan(lo, from(lo, o));
     }
   }
 };
 
-// Scale and zero point of a group from its extremes (hi = max(w, 0), nlo = max(-w, 0), or a NaN).
+// a / D correctly rounded: a (1/D) put right by its remainder (Markstein), above float32's smallest
+// numbers.
+template <int D>
+__device__ __forceinline__ float divide(float a) {
+  constexpr float kD = static_cast<float>(D), kInv = 1.0f / kD;
+  if (a < 1e-30f) return __fdiv_rn(a, kD);
+  const float q = a * kInv;
+  return fmaf(fmaf(-q, kD, a), kInv, q);
+}
+
+// Whole numbers rne(w / s), as float32, for w and s of a 16-bit type: kSnap makes w (1/s) a multiple
+// of 2^-14.  The true quotient (|w / s| < 16) is half-way between two whole numbers, and then comes
+// out so, or 2^-13 and more away from that, since w and s have at most 11 bits; so the second
+// rounding, to a whole number, goes as that of the float32 quotient.
+constexpr float kSnap = 768.0f, kWhole = 12582912.0f;  // 1.5 * 2^9, 1.5 * 2^23
+
+// Whether the reciprocal of s is a normal number, and s is rounded to T finely enough (half a step
+// of 2^-8) that |w / s| stays below 7.5.
 template <typename T>
-__device__ __forceinline__ void group_params(float hi, float nlo, bool affine, T& s, float& z) {
+__device__ __forceinline__ bool plain_scale(float s) {
+  return std::is_same<T, __half>::value ? s >= 6.2e-5f : s >= 1e-30f && s <= 1e30f;
+}
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Scale and zero point of a group from its extremes.
+template <typename T, bool AFFINE>
+__device__ __forceinline__ void group_params(const Extremes<T, AFFINE>& e, T& s, float& z) {
+  const float hi = to_f32(__hmax_nan(e.hi.x, e.hi.y));
+  const float nlo = AFFINE ? -to_f32(__hmin_nan(e.lo.x, e.lo.y)) : 0.0f;
   z = kInt4Zero;
   if (!(hi <= 3.4028235e38f && nlo <= 3.4028235e38f)) {
     s = from_f32<T>(__int_as_float(0x7FC00000));
     return;
   }
-  if (!affine) {
-    s = from_f32<T>(__fdiv_rn(fmaxf(hi, nlo), 7.0f));
+  if (!AFFINE) {
+    s = from_f32<T>(divide<7>(hi));
     return;
   }
-  s = from_f32<T>(__fadd_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(nlo, 15.0f)));
+  s = from_f32<T>(__fadd_rn(divide<15>(hi), divide<15>(nlo)));
   const float sf = to_f32(s);
-  z = sf > 0.0f ? fminf(rintf(__fdiv_rn(nlo, sf)), 15.0f) : 0.0f;
+  z = 0.0f;
+  if (plain_scale<T>(sf))
+    z = (fmaf(nlo, reciprocal(sf), kSnap) + (kWhole - kSnap)) - kWhole;
+  else if (sf > 0.0f)
+    z = rintf(__fdiv_rn(nlo, sf));
+  z = fminf(z, 15.0f);
 }
 
-// Whether the quotients by s can be had from its reciprocal without leaving float32's normal range,
-// and s is rounded to T finely enough (half a step of 2^-8) that |w / s| stays below 7.5.
-template <typename T>
-__device__ __forceinline__ bool plain_scale(float s) {
-  return std::is_same<T, __half>::value ? s >= 6.2e-5f : s >= 1e-30f && s <= 1e30f;
-}
-
-// The word of 8 neighbours, two at a time in the order of the word's halves.  w / s is w (1/s) put
-// right by its remainder (Markstein: the correctly rounded quotient, given the correctly rounded
-// reciprocal); adding 1.5 2^23 rounds it to a whole number, ties to even.  Four codes of a half are
-// one number below 2^16.
+// The word of 8 neighbours, two at a time in the order of the word's halves.  Four codes of a half
+// are one number below 2^16.
 template <typename T, bool AFFINE>
-__device__ __forceinline__ uint32_t encode8(const uint4& v, float s, float inv, float z) {
+__device__ __forceinline__ uint32_t encode8(const uint4& v, float inv, float z) {
   const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-  const uint64_t s2 = f32x2_pack(-s, -s), inv2 = f32x2_pack(inv, inv), k16 = f32x2_pack(16.0f, 16.0f);
-  const uint64_t up = f32x2_pack(12582912.0f, 12582912.0f);
-  const uint64_t down = f32x2_pack(z - 12582912.0f, z - 12582912.0f);
+  const uint64_t inv2 = f32x2_pack(inv, inv), k16 = f32x2_pack(16.0f, 16.0f);
+  const uint64_t snap = f32x2_pack(kSnap, kSnap), up = f32x2_pack(kWhole - kSnap, kWhole - kSnap);
+  const uint64_t down = f32x2_pack(z - kWhole, z - kWhole);
   uint64_t acc = 0;
 #pragma unroll
   for (int j = 3; j >= 0; --j) {
     const float2 f = unpack2<T>(r[j]);
-    const uint64_t w = f32x2_pack(f.x, f.y);
-    uint64_t q = f32x2_mul(w, inv2);
-    q = f32x2_fma(f32x2_fma(q, s2, w), inv2, q);
-    uint64_t u = f32x2_add(f32x2_add(q, up), down);
+    uint64_t u = f32x2_add(f32x2_add(f32x2_fma(f32x2_pack(f.x, f.y), inv2, snap), up), down);
     if (AFFINE) {  // both extremes may have been rounded away from the zero point
       uint32_t x, y;
       f32x2_unpack(u, x, y);
@@ -162,24 +185,20 @@ __global__ void __launch_bounds__(kThreads)
     const int k = at.span * 512 + lane * 16;
     at.next();
     fetch();
-    Extremes<T> e;
+    Extremes<T, AFFINE> e;
     e.start();
     e.add(a.x), e.add(a.y), e.add(a.z), e.add(a.w);
     e.add(b.x), e.add(b.y), e.add(b.z), e.add(b.w);
     e.join(width);
-    const float hx = to_f32(e.hi.x), hy = to_f32(e.hi.y), lx = -to_f32(e.lo.x), ly = -to_f32(e.lo.y);
-    // (a NaN in either half: fmaxf would drop it)
-    const float hi = hx != hx ? hx : hy != hy ? hy : fmaxf(hx, hy);
-    const float nlo = lx != lx ? lx : ly != ly ? ly : fmaxf(lx, ly);
     T s;
     float z;
-    group_params<T>(hi, nlo, AFFINE, s, z);
+    group_params<T, AFFINE>(e, s, z);
     const float sf = to_f32(s);
     uint32_t w0, w1;
     if (plain_scale<T>(sf)) {
-      const float inv = __frcp_rn(sf);
-      w0 = encode8<T, AFFINE>(a, sf, inv, z);
-      w1 = encode8<T, AFFINE>(b, sf, inv, z);
+      const float inv = reciprocal(sf);
+      w0 = encode8<T, AFFINE>(a, inv, z);
+      w1 = encode8<T, AFFINE>(b, inv, z);
     } else {
       w0 = encode8_any<T, AFFINE>(a, sf, z);
       w1 = encode8_any<T, AFFINE>(b, sf, z);
@@ -204,25 +223,22 @@ __global__ void __launch_bounds__(kThreads)
   for (SpanWalk at(groups); at.row < N; at.next()) {
     const int k0 = at.span * group, k1 = static_cast<int>(min(static_cast<long long>(K), static_cast<long long>(k0) + group));
     const uint4* row = reinterpret_cast<const uint4*>(W + at.row * K);
-    Extremes<T> e;
+    Extremes<T, AFFINE> e;
     e.start();
     for (int k = k0 + lane * 8; k < k1; k += 256) {
       const uint4 a = row[k / 8];
       e.add(a.x), e.add(a.y), e.add(a.z), e.add(a.w);
     }
     e.join(32);
-    const float hx = to_f32(e.hi.x), hy = to_f32(e.hi.y), lx = -to_f32(e.lo.x), ly = -to_f32(e.lo.y);
-    const float hi = hx != hx ? hx : hy != hy ? hy : fmaxf(hx, hy);
-    const float nlo = lx != lx ? lx : ly != ly ? ly : fmaxf(lx, ly);
     T s;
     float z;
-    group_params<T>(hi, nlo, AFFINE, s, z);
+    group_params<T, AFFINE>(e, s, z);
     const float sf = to_f32(s);
     const bool plain = plain_scale<T>(sf);
-    const float inv = plain ? __frcp_rn(sf) : 0.0f;
+    const float inv = plain ? reciprocal(sf) : 0.0f;
     uint32_t* out = reinterpret_cast<uint32_t*>(codes + at.row * (K / 2));
     for (int k = k0 + lane * 8; k < k1; k += 256)
-      out[k / 8] = plain ? encode8<T, AFFINE>(row[k / 8], sf, inv, z)
+      out[k / 8] = plain ? encode8<T, AFFINE>(row[k / 8], inv, z)
                          : encode8_any<T, AFFINE>(row[k / 8], sf, z);
     if (lane == 0) {
       scales[at.row * groups + at.span] = s;
