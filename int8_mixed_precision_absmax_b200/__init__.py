@@ -44,6 +44,7 @@ PAIR_TILES = 2        # int8_linear_forward_ex flag: M > 128 products on CTA pai
 # flags of the int4_* calls and the block norms
 _BFLOAT16, _LAYER_NORM, _F32_RESIDUAL, _POST_NORM = 1, 2, 4, 8
 _HALF_TYPES = (torch.float16, torch.bfloat16)
+_ROW_TYPES = _HALF_TYPES + (torch.float32,)
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libint8mm.so")
 _lib = None
@@ -472,46 +473,54 @@ def int8_read_device_status(dev_status: torch.Tensor, stream=None) -> int:
 
 # ------------------------------------------------------------------ 4-bit weights, block norms
 
-def _tensor(t: torch.Tensor, dtype, shape: tuple, like: torch.Tensor, name: str) -> int:
-    """The address of a contiguous CUDA tensor of this dtype and shape on `like`'s device."""
-    if t.dtype != dtype:
+# A small call's time on the host is of the order of its time on the device, so the checks of the
+# calls below are few and flat: one test for each tensor, and the reasons only where it fails.
+
+def _at(t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: int, name: str) -> int:
+    """The address of a contiguous tensor of this dtype and shape on CUDA device `device`."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {like.device}")
-    return t.data_ptr()
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _half(t: torch.Tensor, name: str) -> None:
+def _matrix(t: torch.Tensor, dtypes: tuple, name: str) -> int:
+    """The CUDA device of a contiguous matrix of one of the dtypes."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _HALF_TYPES:
-        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.get_device()
 
 
-def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+def _new(shape, dtype, device: int, stream) -> torch.Tensor:
     """An output tensor whose memory belongs to the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
 
 
-def _call(fn, what: str, like: torch.Tensor, stream, *args) -> None:
-    """fn(*args, stream) with like's device current; raises on a nonzero status."""
-    index = like.get_device()
-    if index == torch.cuda.current_device():
-        status = fn(*args, _stream(stream, index))
+def _call(what: str, device: int, stream, *args) -> None:
+    """The library's function on this device and stream; raises on a nonzero status."""
+    fn = getattr(_lib or load_library(), what)
+    handle = (torch._C._cuda_getCurrentRawStream(device) if stream is None
+              else stream.cuda_stream)
+    if device == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
     else:
-        with torch.cuda.device(index):
-            status = fn(*args, _stream(stream, index))
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
     if status != 0:
         raise Int8mmError(status, what)
 
@@ -528,50 +537,41 @@ def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = 
     [N, K/2] (their order is in int8mm.h), one scale of W's type for every group_size input
     features, and, unless symmetric, one zero point (uint8) for each; zeros is None if
     symmetric."""
-    _half(W, "W")
+    dev = _matrix(W, _HALF_TYPES, "W")
+    T = W.dtype
     N, K = W.shape
-    groups = _int4_shapes(K, group_size)
+    shape = (N, _int4_shapes(K, group_size))
     if symmetric and zeros is not None:
         raise ValueError("zeros is an output of the asymmetric quantizer: pass symmetric=False")
     if codes is None:
-        codes = _new((N, K // 2), torch.uint8, W, stream)
+        codes = _new((N, K // 2), torch.uint8, dev, stream)
     if scales is None:
-        scales = _new((N, groups), W.dtype, W, stream)
+        scales = _new(shape, T, dev, stream)
     if zeros is None and not symmetric:
-        zeros = _new((N, groups), torch.uint8, W, stream)
-    _call(load_library().int4_quant_weight, "int4_quant_weight", W, stream,
-          W.data_ptr(), N, K, group_size, W.dtype is torch.bfloat16,
-          _tensor(codes, torch.uint8, (N, K // 2), W, "codes"),
-          _tensor(scales, W.dtype, (N, groups), W, "scales"),
-          None if symmetric else _tensor(zeros, torch.uint8, (N, groups), W, "zeros"))
+        zeros = _new(shape, torch.uint8, dev, stream)
+    _call("int4_quant_weight", dev, stream, W.data_ptr(), N, K, group_size, T is torch.bfloat16,
+          _at(codes, torch.uint8, (N, K // 2), dev, "codes"), _at(scales, T, shape, dev, "scales"),
+          None if symmetric else _at(zeros, torch.uint8, shape, dev, "zeros"))
     return codes, scales, zeros
-
-
-def _int4_operands(codes, scales, zeros, group_size: int):
-    """(N, K, addresses) of a 4-bit weight, checked against each other."""
-    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
-        raise TypeError("codes must be a CUDA tensor")
-    if scales.dtype not in _HALF_TYPES:
-        raise TypeError(f"scales must be torch.float16 or torch.bfloat16, got {scales.dtype}")
-    if codes.dim() != 2:
-        raise ValueError("codes must have 2 dimensions")
-    N, K = codes.shape[0], codes.shape[1] * 2
-    shape = (N, _int4_shapes(K, group_size))
-    return (N, K, _tensor(codes, torch.uint8, codes.shape, codes, "codes"),
-            _tensor(scales, scales.dtype, shape, codes, "scales"),
-            None if zeros is None else _tensor(zeros, torch.uint8, shape, codes, "zeros"))
 
 
 def int4_dequant_weight(codes: torch.Tensor, scales: torch.Tensor,
                         zeros: torch.Tensor | None = None, group_size: int = 128,
                         W_hat: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """What the codes stand for: scales * (code - zero) of scales' type, [N, K]."""
-    N, K, c, s, z = _int4_operands(codes, scales, zeros, group_size)
+    dev = _matrix(codes, (torch.uint8,), "codes")
+    N, K = codes.shape
+    K *= 2
+    T = scales.dtype
+    if T not in _HALF_TYPES:
+        raise TypeError(f"scales must be torch.float16 or torch.bfloat16, got {T}")
+    shape = (N, _int4_shapes(K, group_size))
     if W_hat is None:
-        W_hat = _new((N, K), scales.dtype, codes, stream)
-    _call(load_library().int4_dequant_weight, "int4_dequant_weight", codes, stream, c, s, z, N, K,
-          group_size, scales.dtype is torch.bfloat16,
-          _tensor(W_hat, scales.dtype, (N, K), codes, "W_hat"))
+        W_hat = _new((N, K), T, dev, stream)
+    _call("int4_dequant_weight", dev, stream, codes.data_ptr(),
+          _at(scales, T, shape, dev, "scales"),
+          None if zeros is None else _at(zeros, torch.uint8, shape, dev, "zeros"), N, K,
+          group_size, T is torch.bfloat16, _at(W_hat, T, (N, K), dev, "W_hat"))
     return W_hat
 
 
@@ -581,34 +581,20 @@ def int4_linear_forward(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
                         dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X . W_hat^T + bias, [M, N] of X's type (fp16 or bf16), on the 4-bit weights of
     int4_quant_weight.  dev_status: an int32 that receives a device-side failure code."""
-    _half(X, "X")
-    N, K, c, s, z = _int4_operands(codes, scales, zeros, group_size)
+    dev = _matrix(X, _HALF_TYPES, "X")
     T = X.dtype
-    M = X.shape[0]
-    if scales.dtype is not T:
-        raise TypeError(f"scales must be {T} like X, got {scales.dtype}")
-    if X.shape[1] != K:
-        raise ValueError(f"X must have {K} columns, got {X.shape[1]}")
+    M, K = X.shape
+    N = codes.shape[0]
+    shape = (N, _int4_shapes(K, group_size))
     if Y is None:
-        Y = _new((M, N), T, X, stream)
-    _call(load_library().int4_linear_forward, "int4_linear_forward", X, stream,
-          _tensor(X, T, X.shape, codes, "X"), M, K, c, s, z,
-          None if bias is None else _tensor(bias, T, (N,), codes, "bias"), N, group_size,
-          T is torch.bfloat16, _tensor(Y, T, (M, N), codes, "Y"),
-          None if dev_status is None
-          else _tensor(dev_status, torch.int32, (1,), codes, "dev_status"))
+        Y = _new((M, N), T, dev, stream)
+    _call("int4_linear_forward", dev, stream, X.data_ptr(), M, K,
+          _at(codes, torch.uint8, (N, K // 2), dev, "codes"), _at(scales, T, shape, dev, "scales"),
+          None if zeros is None else _at(zeros, torch.uint8, shape, dev, "zeros"),
+          None if bias is None else _at(bias, T, (N,), dev, "bias"), N, group_size,
+          T is torch.bfloat16, _at(Y, T, (M, N), dev, "Y"),
+          None if dev_status is None else _at(dev_status, torch.int32, (1,), dev, "dev_status"))
     return Y
-
-
-def _rows(x: torch.Tensor, name: str) -> None:
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if x.dtype not in _HALF_TYPES and x.dtype is not torch.float32:
-        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def int8_block_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -618,24 +604,21 @@ def int8_block_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     """h = norm(x) * weight + bias for the rows of x [M, D]: the root-mean-square norm, or the
     layer norm (layer_norm=True).  x is fp16, bf16, or float32 (a residual stream kept in 32
     bits; h then has the type of weight, or of the h given, or fp16).  h may be x itself."""
-    _rows(x, "x")
+    dev = _matrix(x, _ROW_TYPES, "x")
+    T = R = x.dtype
     M, D = x.shape
-    if x.dtype is not torch.float32:
-        T = x.dtype
-    elif weight is not None:
-        T = weight.dtype
-    else:
-        T = torch.float16 if h is None else h.dtype
-    if T not in _HALF_TYPES:
-        raise TypeError(f"weight and h must be torch.float16 or torch.bfloat16, got {T}")
+    if R is torch.float32:
+        T = weight.dtype if weight is not None else torch.float16 if h is None else h.dtype
+        if T not in _HALF_TYPES:
+            raise TypeError(f"weight and h must be torch.float16 or torch.bfloat16, got {T}")
     if h is None:
-        h = _new((M, D), T, x, stream)
+        h = _new((M, D), T, dev, stream)
     flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
-             | (_F32_RESIDUAL if x.dtype is torch.float32 else 0))
-    _call(load_library().int8_block_norm, "int8_block_norm", x, stream, x.data_ptr(), M, D,
-          None if weight is None else _tensor(weight, T, (D,), x, "weight"),
-          None if bias is None else _tensor(bias, T, (D,), x, "bias"), eps, flags,
-          _tensor(h, T, (M, D), x, "h"))
+             | (0 if R is T else _F32_RESIDUAL))
+    _call("int8_block_norm", dev, stream, x.data_ptr(), M, D,
+          None if weight is None else _at(weight, T, (D,), dev, "weight"),
+          None if bias is None else _at(bias, T, (D,), dev, "bias"), eps, flags,
+          _at(h, T, (M, D), dev, "h"))
     return h
 
 
@@ -654,37 +637,39 @@ def int8_block_residual(f: torch.Tensor, x: torch.Tensor, post_norm: bool = Fals
 
     f is fp16 or bf16; x has f's type or is float32, and y has x's.  gate is [Gr, D] or [D]: row
     m of f takes gate row m // (M / Gr).  y may be x itself, h may be f itself."""
-    _half(f, "f")
-    _rows(x, "x")
+    dev = _matrix(f, _HALF_TYPES, "f")
     T, R = f.dtype, x.dtype
-    M, D = f.shape
+    rows = M, D = f.shape
+    vector = (D,)
     if R is not T and R is not torch.float32:
         raise TypeError(f"x must be {T} like f, or float32, got {R}")
     if not post_norm and (post_weight is not None or post_bias is not None):
         raise ValueError("post_weight and post_bias need post_norm=True")
     if not next_norm and (next_weight is not None or next_bias is not None or h is not None):
         raise ValueError("next_weight, next_bias and h need next_norm=True")
-    gate_rows = 0
+    gate_rows, gate_at = 0, None
     if gate is not None:
-        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
-        if gate_rows <= 0 or M % gate_rows:
-            raise ValueError(f"gate has {gate_rows} rows, which do not divide the {M} rows of f")
+        if gate.dim() == 2:
+            gate_rows = gate.shape[0]
+            if gate_rows <= 0 or M % gate_rows:
+                raise ValueError(f"gate has {gate_rows} rows, which do not divide the {M} rows "
+                                 "of f")
+            gate_at = _at(gate, T, (gate_rows, D), dev, "gate")
+        else:
+            gate_rows, gate_at = 1, _at(gate, T, vector, dev, "gate")
     if y is None:
-        y = _new((M, D), R, f, stream)
+        y = _new(rows, R, dev, stream)
     if h is None and next_norm:
-        h = _new((M, D), T, f, stream)
+        h = _new(rows, T, dev, stream)
     flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
-             | (_F32_RESIDUAL if R is not T else 0) | (_POST_NORM if post_norm else 0))
-    _call(load_library().int8_block_residual, "int8_block_residual", f, stream, f.data_ptr(),
-          _tensor(x, R, (M, D), f, "x"), M, D,
-          None if post_weight is None else _tensor(post_weight, T, (D,), f, "post_weight"),
-          None if post_bias is None else _tensor(post_bias, T, (D,), f, "post_bias"),
-          None if gate is None
-          else _tensor(gate, T, (gate_rows, D) if gate.dim() == 2 else (D,), f, "gate"),
-          gate_rows, x_scale, f_scale,
-          None if next_weight is None else _tensor(next_weight, T, (D,), f, "next_weight"),
-          None if next_bias is None else _tensor(next_bias, T, (D,), f, "next_bias"), eps, flags,
-          _tensor(y, R, (M, D), f, "y"), None if h is None else _tensor(h, T, (M, D), f, "h"))
+             | (0 if R is T else _F32_RESIDUAL) | (_POST_NORM if post_norm else 0))
+    _call("int8_block_residual", dev, stream, f.data_ptr(), _at(x, R, rows, dev, "x"), M, D,
+          None if post_weight is None else _at(post_weight, T, vector, dev, "post_weight"),
+          None if post_bias is None else _at(post_bias, T, vector, dev, "post_bias"),
+          gate_at, gate_rows, x_scale, f_scale,
+          None if next_weight is None else _at(next_weight, T, vector, dev, "next_weight"),
+          None if next_bias is None else _at(next_bias, T, vector, dev, "next_bias"), eps, flags,
+          _at(y, R, rows, dev, "y"), None if h is None else _at(h, T, rows, dev, "h"))
     return y, h
 
 
