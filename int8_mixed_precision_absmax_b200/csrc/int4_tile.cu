@@ -32,9 +32,8 @@ namespace {
 constexpr int kTileN = 128;   // channels per tile
 constexpr int kStepK = 128;   // k per step
 constexpr int kCodeBytes = kTileN * kStepK / 2;
-constexpr int kDequantWarps = 8, kEpiWarps = 4;
-constexpr int kTmaWarp = kDequantWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kTeamWarps = 8, kEpiWarps = 4;  // the warps that dequantize one step
+__host__ __device__ constexpr int threads_of(int teams) { return (teams * kTeamWarps + kEpiWarps + 2) * 32; }
 constexpr int kMaxStages = 10, kMaxA = 4;
 constexpr int kACols = kStepK / 2;  // tensor-memory columns of a step of W_hat
 
@@ -157,8 +156,8 @@ __host__ __device__ constexpr uint32_t tile_idesc(int n) {
 
 }  // namespace
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int TEAMS>
+__global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
     int4_tile_kernel(const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const TileArgs p) {
   extern __shared__ uint8_t tile_smem_raw[];
@@ -166,6 +165,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       (reinterpret_cast<uintptr_t>(tile_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int sbytes = stage_bytes(p.tn);
   TileShared& S = *reinterpret_cast<TileShared*>(ring + p.stages * sbytes);
+  constexpr int kDequantWarps = TEAMS * kTeamWarps;
+  constexpr int kTmaWarp = kDequantWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&S.empty[s], 1);
     }
     for (int s = 0; s < p.a_stages; ++s) {
-      mbar_init(&S.a_full[s], kDequantWarps);
+      mbar_init(&S.a_full[s], kTeamWarps);
       mbar_init(&S.a_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -268,13 +269,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok) report(p.status);
     }
   } else if (warp < kDequantWarps) {
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, half = warp >> 2 & 1, team = warp / kTeamWarps;
     const int row = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     // the two 16-byte chunks of this thread's 32 bytes, under the 64-byte swizzle
     const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
     const uint32_t off0 = row * 64 + ((2u * half) ^ swz) * 16, off1 = row * 64 + ((2u * half + 1) ^ swz) * 16;
-    int stage = 0, as = 0;
+    int stage = 0, as = 0, turn = 0;  // the teams take steps in turn
     uint32_t phase = 0, a_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
       const long long n = min(t / p.m_tiles * kTileN + row, p.N - 1);
@@ -283,6 +284,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       GroupChunk cur = {}, nxt = {};
       int held = -1;  // first group of cur
       for (int k = k_begin; k < k_end; ++k) {
+        const int s_now = stage, a_now = as;
+        const uint32_t ph_now = phase, a_ph_now = a_phase;
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
+        const bool mine = turn == team;
+        if (++turn == TEAMS) turn = 0;
+        if (!mine) continue;
         const int g = (k * kStepK + half * 64) / p.group;
         const int chunk = g & ~7;
         if (chunk != held) {
@@ -291,8 +299,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           held = chunk;
           load_chunk<T>(nxt, srow, zrow, chunk + 8, p.groups);
         }
-        if (!warp_wait(&S.full[stage], phase, abort)) { ok = false; break; }
-        const uint8_t* codes = ring + stage * sbytes;
+        // With two teams the stage's last step may be the other team's: only once that step has been
+        // multiplied is the barrier's phase the one before this step's.
+        if (TEAMS > 1 && !warp_wait(&S.empty[s_now], ph_now ^ 1u, abort)) { ok = false; break; }
+        if (!warp_wait(&S.full[s_now], ph_now, abort)) { ok = false; break; }
+        const uint8_t* codes = ring + s_now * sbytes;
         const uint4 c0 = *reinterpret_cast<const uint4*>(codes + off0);
         const uint4 c1 = *reinterpret_cast<const uint4*>(codes + off1);
         Int4Values<T> q;
@@ -308,15 +319,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         q.word(c1.y, out + 20);
         q.word(c1.z, out + 24);
         q.word(c1.w, out + 28);
-        if (!warp_wait(&S.a_empty[as], a_phase ^ 1u, abort)) { ok = false; break; }
+        if (!warp_wait(&S.a_empty[a_now], a_ph_now ^ 1u, abort)) { ok = false; break; }
         tc_fence_after();
-        tmem_st32(a_base + static_cast<uint32_t>(as * kACols + half * 32) + lane_base, out);
+        tmem_st32(a_base + static_cast<uint32_t>(a_now * kACols + half * 32) + lane_base, out);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.a_full[as]);
-        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-        if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
+        if (lane == 0) mbar_arrive(&S.a_full[a_now]);
       }
     }
     if (!ok) report(p.status);
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int m0 = t0 % p.m_tiles * p.tn, n0 = t0 / p.m_tiles * kTileN;
       const int c_begin = p.tn * split / p.splits, c_end = p.tn * (split + 1) / p.splits;
       const uint32_t base = smem_addr(ring);
-      for (int i = c_begin * kTileN + static_cast<int>(threadIdx.x); i < c_end * kTileN; i += kThreads) {
+      for (int i = c_begin * kTileN + static_cast<int>(threadIdx.x); i < c_end * kTileN; i += threads_of(TEAMS)) {
         const long long m = m0 + i / kTileN;
         const int n = n0 + i % kTileN;
         if (m >= p.M || n >= p.N) continue;
@@ -470,13 +479,14 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
   p.steps = (w.K + kStepK - 1) / kStepK;
-  cudaError_t e = cudaFuncSetAttribute(int4_tile_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const int teams = t.tmem_cols == 512 ? 2 : 1;
+  auto kernel = teams == 2 ? int4_tile_kernel<T, 2> : int4_tile_kernel<T, 1>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(226 * 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(t.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(teams));
   cfg.dynamicSmemBytes = t.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -487,7 +497,7 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = t.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, int4_tile_kernel<T>, map_x, map_w, p);
+  return cudaLaunchKernelEx(&cfg, kernel, map_x, map_w, p);
 }
 
 }  // namespace
