@@ -61,14 +61,25 @@ struct TileShared {  // behind the ring
 __host__ __device__ constexpr int slot_cols(int tn) { return (tn + 31) / 32 * 32; }
 __host__ __device__ constexpr int stage_bytes(int tn) { return kCodeBytes + tn * kStepK * 2; }
 
+// One lane of a converged warp, the same each time.  Where the rest of a step's code is the whole
+// warp's, the MMAs' descriptors stay in uniform registers; issued from a branch on the lane's number
+// the 8 of a step took 500 to 800 cycles, more than their 256 columns take to multiply.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, float32 sums.  Issued by one thread.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+                                       bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
@@ -233,41 +244,44 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
       if (!ok) report(p.status);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t idesc = tile_idesc<T>(p.tn);
-      int stage = 0, as = 0, slot = 0;
-      uint32_t phase = 0, a_phase = 0, d_phase = 0;
-      for (int t = t0; ok && t < p.tiles; t += dt) {
-        if (!mbar_wait_bounded(&S.d_empty[slot], d_phase ^ 1u, abort)) { ok = false; break; }
+    const uint32_t idesc = tile_idesc<T>(p.tn);
+    const uint64_t b0 = sw128_kmajor_desc(smem_addr(ring + kCodeBytes));  // of stage 0; in 16 bytes:
+    const uint32_t b_stage = static_cast<uint32_t>(sbytes) >> 4, b_half = static_cast<uint32_t>(p.tn) * 8;
+    int stage = 0, as = 0, slot = 0;
+    uint32_t phase = 0, a_phase = 0, d_phase = 0;
+    for (int t = t0; ok && t < p.tiles; t += dt) {
+      if (!warp_wait(&S.d_empty[slot], d_phase ^ 1u, abort)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(slot * slot_cols(p.tn));
+      for (int k = k_begin; k < k_end; ++k) {
+        if (!warp_wait(&S.full[stage], phase, abort) || !warp_wait(&S.a_full[as], a_phase, abort)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(slot * slot_cols(p.tn));
-        for (int k = k_begin; k < k_end; ++k) {
-          if (!mbar_wait_bounded(&S.full[stage], phase, abort) ||
-              !mbar_wait_bounded(&S.a_full[as], a_phase, abort)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = a_base + static_cast<uint32_t>(as * kACols);
-          const uint32_t b = smem_addr(ring + stage * sbytes + kCodeBytes);
+        const uint32_t a = a_base + static_cast<uint32_t>(as * kACols);
+        const uint64_t b = b0 + static_cast<uint32_t>(stage) * b_stage;
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kStepK / 16; ++j)
-            mma_ts(d, a + 8u * j, sw128_kmajor_desc(b + (j / 4) * p.tn * 128 + (j % 4) * 32), idesc,
-                   (k > k_begin || j > 0) ? 1u : 0u);
+            mma_ts(d, a + 8u * j, b + (j / 4) * b_half + (j % 4) * 2, idesc, k > k_begin || j > 0);
           mma_commit(&S.empty[stage]);
           mma_commit(&S.a_empty[as]);
-          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-          if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
         }
-        if (!ok) break;
-        mma_commit(&S.d_full[slot]);
-        if (++slot == p.d_slots) { slot = 0; d_phase ^= 1u; }
+        __syncwarp();
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
       }
-      mma_commit(&S.drain);  // every MMA is done before tensor memory is freed
-      int dummy = 0;
-      mbar_wait_bounded(&S.drain, 0, &dummy);
-      if (!ok) report(p.status);
+      if (!ok) break;
+      if (elect_one()) mma_commit(&S.d_full[slot]);
+      __syncwarp();
+      if (++slot == p.d_slots) { slot = 0; d_phase ^= 1u; }
     }
+    if (elect_one()) mma_commit(&S.drain);  // every MMA is done before tensor memory is freed
+    __syncwarp();
+    int dummy = 0;
+    mbar_wait_bounded(&S.drain, 0, &dummy);
+    if (!ok && lane == 0) report(p.status);
   } else if (warp < kDequantWarps) {
     const int quad = warp & 3, half = warp >> 2 & 1, team = warp / kTeamWarps;
     const int row = quad * 32 + lane;
@@ -275,6 +289,8 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
     // the two 16-byte chunks of this thread's 32 bytes, under the 64-byte swizzle
     const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
     const uint32_t off0 = row * 64 + ((2u * half) ^ swz) * 16, off1 = row * 64 + ((2u * half + 1) ^ swz) * 16;
+    const int g_mul = kStepK / p.group, g_half = half * 64 / p.group;
+    const int g_steps = p.group < kStepK ? 1 : p.group / kStepK;
     int stage = 0, as = 0, turn = 0;  // the teams take steps in turn
     uint32_t phase = 0, a_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
@@ -283,15 +299,22 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
       const uint8_t* zrow = p.zeros ? p.zeros + n * p.groups : nullptr;
       GroupChunk cur = {}, nxt = {};
       int held = -1;  // first group of cur
+      // this half of step k: group k g_mul + g_half where a step holds several, otherwise one group
+      // for every g_steps steps, the next of them in g_left
+      int g_long = k_begin / g_steps, g_left = g_steps - k_begin % g_steps;
       for (int k = k_begin; k < k_end; ++k) {
         const int s_now = stage, a_now = as;
         const uint32_t ph_now = phase, a_ph_now = a_phase;
         if (++stage == p.stages) { stage = 0; phase ^= 1u; }
         if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
+        const int g = p.group < kStepK ? k * g_mul + g_half : g_long;
+        if (--g_left == 0) {
+          g_left = g_steps;
+          ++g_long;
+        }
         const bool mine = turn == team;
         if (++turn == TEAMS) turn = 0;
         if (!mine) continue;
-        const int g = (k * kStepK + half * 64) / p.group;
         const int chunk = g & ~7;
         if (chunk != held) {
           if (chunk == held + 8 && held >= 0) cur = nxt;
