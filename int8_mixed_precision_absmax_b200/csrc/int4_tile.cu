@@ -49,6 +49,7 @@ struct TileArgs {
 };
 
 struct TileShared {  // behind the ring
+  uint4 turn[kEpiWarps][16 * 32 * 2 / 16];
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t a_full[kMaxA], a_empty[kMaxA];
   uint64_t d_full[2], d_empty[2];
@@ -365,15 +366,32 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
       const float b = (p.bias && n_ok) ? to_f32(static_cast<const T*>(p.bias)[n]) : 0.0f;
       float* part = reinterpret_cast<float*>(ring);  // splits > 1: the ring is drained
       T* Y = static_cast<T*>(p.Y);
+      T* turned = reinterpret_cast<T*>(S.turn[quad]);  // 16 tokens x the warp's 32 channels
+      const bool vectors = p.N % 8 == 0;
+      const uint32_t d = tmem + static_cast<uint32_t>(slot * slot_cols(p.tn)) + lane_base;
       for (int c = 0; c < p.tn; c += 16) {
         uint32_t r[16];
         __syncwarp();
-        tmem_ld16(tmem + static_cast<uint32_t>(slot * slot_cols(p.tn) + c) + lane_base, r);
+        tmem_ld16(d + static_cast<uint32_t>(c), r);
         tmem_ld_wait();
         if (p.splits > 1) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             part[(c + j) * kTileN + quad * 32 + lane] = __uint_as_float(r[j]);
+        } else if (vectors) {
+          // a lane has one channel of 16 tokens: through shared memory to 8 channels of one token
+#pragma unroll
+          for (int j = 0; j < 16; ++j) turned[j * 32 + lane] = from_f32<T>(__uint_as_float(r[j]) + b);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = lane / 4 + 8 * i;
+            const long long m = m0 + c + j;
+            const int n8 = n - lane + lane % 4 * 8;
+            if (m < p.M && n8 < p.N)
+              *reinterpret_cast<uint4*>(Y + m * p.N + n8) =
+                  *reinterpret_cast<const uint4*>(turned + j * 32 + lane % 4 * 8);
+          }
         } else if (n_ok) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
