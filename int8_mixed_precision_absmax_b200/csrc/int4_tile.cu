@@ -84,19 +84,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -292,6 +279,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
     const uint32_t off0 = row * 64 + ((2u * half) ^ swz) * 16, off1 = row * 64 + ((2u * half + 1) ^ swz) * 16;
     const int g_mul = kStepK / p.group, g_half = half * 64 / p.group;
     const int g_steps = p.group < kStepK ? 1 : p.group / kStepK;
+    const bool odd_stages = TEAMS > 1 && p.stages % TEAMS != 0;
     int stage = 0, as = 0, turn = 0;  // the teams take steps in turn
     uint32_t phase = 0, a_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
@@ -323,29 +311,31 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
           held = chunk;
           load_chunk<T>(nxt, srow, zrow, chunk + 8, p.groups);
         }
-        // With two teams the stage's last step may be the other team's: only once that step has been
-        // multiplied is the barrier's phase the one before this step's.
-        if (TEAMS > 1 && !warp_wait(&S.empty[s_now], ph_now ^ 1u, abort)) { ok = false; break; }
+        // Where the stage's last step was the other team's: only once that has been multiplied is the
+        // barrier's phase the one before this step's.
+        if (odd_stages && !warp_wait(&S.empty[s_now], ph_now ^ 1u, abort)) { ok = false; break; }
         if (!warp_wait(&S.full[s_now], ph_now, abort)) { ok = false; break; }
         const uint8_t* codes = ring + s_now * sbytes;
         const uint4 c0 = *reinterpret_cast<const uint4*>(codes + off0);
         const uint4 c1 = *reinterpret_cast<const uint4*>(codes + off1);
         Int4Values<T> q;
-        uint32_t out[32];
+        uint32_t out[16];
         q.set(chunk_scale2(cur, g & 7), zrow ? chunk_zero(cur, g & 7) : kInt4Zero);
         q.word(c0.x, out);
         q.word(c0.y, out + 4);
         q.word(c0.z, out + 8);
         q.word(c0.w, out + 12);
-        if (p.group == 32)  // the second 32 of the 64 k: the next group (g is even)
-          q.set(chunk_scale2(cur, (g + 1) & 7), zrow ? chunk_zero(cur, (g + 1) & 7) : kInt4Zero);
-        q.word(c1.x, out + 16);
-        q.word(c1.y, out + 20);
-        q.word(c1.z, out + 24);
-        q.word(c1.w, out + 28);
         if (!warp_wait(&S.a_empty[a_now], a_ph_now ^ 1u, abort)) { ok = false; break; }
         tc_fence_after();
-        tmem_st32(a_base + static_cast<uint32_t>(a_now * kACols + half * 32) + lane_base, out);
+        const uint32_t to = a_base + static_cast<uint32_t>(a_now * kACols + half * 32) + lane_base;
+        tmem_st16(to, out);
+        if (p.group == 32)  // the second 32 of the 64 k: the next group (g is even)
+          q.set(chunk_scale2(cur, (g + 1) & 7), zrow ? chunk_zero(cur, (g + 1) & 7) : kInt4Zero);
+        q.word(c1.x, out);
+        q.word(c1.y, out + 4);
+        q.word(c1.z, out + 8);
+        q.word(c1.w, out + 12);
+        tmem_st16(to + 16, out);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -440,7 +430,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
 namespace {
 
 struct TilePlan {
-  int tn, stages, a_stages, d_slots, tmem_cols, splits, grid;
+  int tn, stages, a_stages, d_slots, tmem_cols, splits, teams, grid;
   size_t smem;
 };
 
@@ -451,14 +441,13 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
   if (M <= 128) {
     t.tn = (M + 15) / 16 * 16;
   } else {
-    // the width that needs the least time in waves of one tile per SM
+    // The width that needs the least time: waves of one tile per SM, each of a time that grows with
+    // tn + 90 (2048 x 11008 x 4096: 154 us in 5 waves of 256, 171 in 7 of 192, 193 in 10 of 128).
     t.tn = 256;
     long long best = -1;
-    for (int tn = 256; tn >= 64; tn -= 16) {
-      const int per_sm = tn <= 128 ? 2 : 1;
+    for (int tn = 256; tn > 128; tn -= 16) {
       const long long tiles = static_cast<long long>((M + tn - 1) / tn) * n_tiles;
-      const long long waves = (tiles + num_sms * per_sm - 1) / (num_sms * per_sm);
-      const long long cost = waves * per_sm * (tn + 24);
+      const long long cost = (tiles + num_sms - 1) / num_sms * (tn + 90);
       if (best < 0 || cost < best) best = cost, t.tn = tn;
     }
   }
@@ -474,6 +463,7 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
     if (t.splits < 1) t.splits = 1;
   }
   t.tmem_cols = per_sm == 2 ? 256 : 512;
+  t.teams = per_sm == 2 ? 1 : 2;
   t.d_slots = (t.splits == 1 && 2 * slot_cols(t.tn) + 2 * kACols <= t.tmem_cols) ? 2 : 1;
   t.a_stages = (t.tmem_cols - t.d_slots * slot_cols(t.tn)) / kACols;
   if (t.a_stages > kMaxA) t.a_stages = kMaxA;
@@ -520,14 +510,13 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
   p.steps = (w.K + kStepK - 1) / kStepK;
-  const int teams = t.tmem_cols == 512 ? 2 : 1;
-  auto kernel = teams == 2 ? int4_tile_kernel<T, 2> : int4_tile_kernel<T, 1>;
+  auto kernel = t.teams == 2 ? int4_tile_kernel<T, 2> : int4_tile_kernel<T, 1>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(226 * 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(t.grid);
-  cfg.blockDim = dim3(threads_of(teams));
+  cfg.blockDim = dim3(threads_of(t.teams));
   cfg.dynamicSmemBytes = t.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
