@@ -32,8 +32,8 @@ namespace {
 constexpr int kTileN = 128;   // channels per tile
 constexpr int kStepK = 128;   // k per step
 constexpr int kCodeBytes = kTileN * kStepK / 2;
-constexpr int kTeamWarps = 8, kEpiWarps = 4;  // the warps that dequantize one step
-__host__ __device__ constexpr int threads_of(int teams) { return (teams * kTeamWarps + kEpiWarps + 2) * 32; }
+constexpr int kTeams = 2, kEpiWarps = 4;  // teams of warps that dequantize the steps in turn
+__host__ __device__ constexpr int threads_of(int team_warps) { return (kTeams * team_warps + kEpiWarps + 2) * 32; }
 constexpr int kMaxStages = 10, kMaxA = 4;
 constexpr int kACols = kStepK / 2;  // tensor-memory columns of a step of W_hat
 
@@ -155,8 +155,10 @@ __host__ __device__ constexpr uint32_t tile_idesc(int n) {
 
 }  // namespace
 
-template <typename T, int TEAMS>
-__global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
+// TW warps dequantize a step: 4 where two blocks share an SM, each warp all of a step's k for its 32
+// channels; 8 where a block has the SM to itself, each half of them.
+template <typename T, int TW>
+__global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     int4_tile_kernel(const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const TileArgs p) {
   extern __shared__ uint8_t tile_smem_raw[];
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
       (reinterpret_cast<uintptr_t>(tile_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int sbytes = stage_bytes(p.tn);
   TileShared& S = *reinterpret_cast<TileShared*>(ring + p.stages * sbytes);
-  constexpr int kDequantWarps = TEAMS * kTeamWarps;
+  constexpr int kDequantWarps = kTeams * TW;
   constexpr int kTmaWarp = kDequantWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
       mbar_init(&S.empty[s], 1);
     }
     for (int s = 0; s < p.a_stages; ++s) {
-      mbar_init(&S.a_full[s], kTeamWarps);
+      mbar_init(&S.a_full[s], TW);
       mbar_init(&S.a_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -271,15 +273,14 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
     mbar_wait_bounded(&S.drain, 0, &dummy);
     if (!ok && lane == 0) report(p.status);
   } else if (warp < kDequantWarps) {
-    const int quad = warp & 3, half = warp >> 2 & 1, team = warp / kTeamWarps;
+    constexpr int kChunks = TW == 4 ? 4 : 2;  // of 32 k: 16 bytes of a row's codes
+    const int quad = warp & 3, first = TW == 4 ? 0 : (warp >> 2 & 1) * kChunks, team = warp / TW;
     const int row = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    // the two 16-byte chunks of this thread's 32 bytes, under the 64-byte swizzle
-    const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
-    const uint32_t off0 = row * 64 + ((2u * half) ^ swz) * 16, off1 = row * 64 + ((2u * half + 1) ^ swz) * 16;
-    const int g_mul = kStepK / p.group, g_half = half * 64 / p.group;
+    const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);  // of the 64-byte swizzle
+    const int g_mul = kStepK / p.group, g_half = first * 32 / p.group;
     const int g_steps = p.group < kStepK ? 1 : p.group / kStepK;
-    const bool odd_stages = TEAMS > 1 && p.stages % TEAMS != 0;
+    const bool odd_stages = p.stages % kTeams != 0;
     int stage = 0, as = 0, turn = 0;  // the teams take steps in turn
     uint32_t phase = 0, a_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
           ++g_long;
         }
         const bool mine = turn == team;
-        if (++turn == TEAMS) turn = 0;
+        if (++turn == kTeams) turn = 0;
         if (!mine) continue;
         const int chunk = g & ~7;
         if (chunk != held) {
@@ -316,26 +317,27 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
         if (odd_stages && !warp_wait(&S.empty[s_now], ph_now ^ 1u, abort)) { ok = false; break; }
         if (!warp_wait(&S.full[s_now], ph_now, abort)) { ok = false; break; }
         const uint8_t* codes = ring + s_now * sbytes;
-        const uint4 c0 = *reinterpret_cast<const uint4*>(codes + off0);
-        const uint4 c1 = *reinterpret_cast<const uint4*>(codes + off1);
+        const uint32_t to = a_base + static_cast<uint32_t>(a_now * kACols + first * 16) + lane_base;
         Int4Values<T> q;
-        uint32_t out[16];
-        q.set(chunk_scale2(cur, g & 7), zrow ? chunk_zero(cur, g & 7) : kInt4Zero);
-        q.word(c0.x, out);
-        q.word(c0.y, out + 4);
-        q.word(c0.z, out + 8);
-        q.word(c0.w, out + 12);
-        if (!warp_wait(&S.a_empty[a_now], a_ph_now ^ 1u, abort)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t to = a_base + static_cast<uint32_t>(a_now * kACols + half * 32) + lane_base;
-        tmem_st16(to, out);
-        if (p.group == 32)  // the second 32 of the 64 k: the next group (g is even)
-          q.set(chunk_scale2(cur, (g + 1) & 7), zrow ? chunk_zero(cur, (g + 1) & 7) : kInt4Zero);
-        q.word(c1.x, out);
-        q.word(c1.y, out + 4);
-        q.word(c1.z, out + 8);
-        q.word(c1.w, out + 12);
-        tmem_st16(to + 16, out);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          // a new group for every chunk of 32, every second one, or none within the step's part
+          const int gc = (g & 7) + (p.group == 32 ? c : p.group == 64 ? c / 2 : 0);
+          if (c == 0 || p.group == 32 || (p.group == 64 && c == 2))
+            q.set(chunk_scale2(cur, gc), zrow ? chunk_zero(cur, gc) : kInt4Zero);
+          const uint4 w = *reinterpret_cast<const uint4*>(codes + row * 64 + ((first + c) ^ swz) * 16);
+          uint32_t out[16];
+          q.word(w.x, out);
+          q.word(w.y, out + 4);
+          q.word(w.z, out + 8);
+          q.word(w.w, out + 12);
+          if (c == 0) {
+            if (!warp_wait(&S.a_empty[a_now], a_ph_now ^ 1u, abort)) { ok = false; break; }
+            tc_fence_after();
+          }
+          tmem_st16(to + 16 * c, out);
+        }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
       const int m0 = t0 % p.m_tiles * p.tn, n0 = t0 / p.m_tiles * kTileN;
       const int c_begin = p.tn * split / p.splits, c_end = p.tn * (split + 1) / p.splits;
       const uint32_t base = smem_addr(ring);
-      for (int i = c_begin * kTileN + static_cast<int>(threadIdx.x); i < c_end * kTileN; i += threads_of(TEAMS)) {
+      for (int i = c_begin * kTileN + static_cast<int>(threadIdx.x); i < c_end * kTileN; i += threads_of(TW)) {
         const long long m = m0 + i / kTileN;
         const int n = n0 + i % kTileN;
         if (m >= p.M || n >= p.N) continue;
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(threads_of(TEAMS), TEAMS == 1 ? 2 : 1)
 namespace {
 
 struct TilePlan {
-  int tn, stages, a_stages, d_slots, tmem_cols, splits, teams, grid;
+  int tn, stages, a_stages, d_slots, tmem_cols, splits, team_warps, grid;
   size_t smem;
 };
 
@@ -463,7 +465,7 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
     if (t.splits < 1) t.splits = 1;
   }
   t.tmem_cols = per_sm == 2 ? 256 : 512;
-  t.teams = per_sm == 2 ? 1 : 2;
+  t.team_warps = per_sm == 2 ? 4 : 8;
   t.d_slots = (t.splits == 1 && 2 * slot_cols(t.tn) + 2 * kACols <= t.tmem_cols) ? 2 : 1;
   t.a_stages = (t.tmem_cols - t.d_slots * slot_cols(t.tn)) / kACols;
   if (t.a_stages > kMaxA) t.a_stages = kMaxA;
@@ -510,13 +512,13 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
   p.steps = (w.K + kStepK - 1) / kStepK;
-  auto kernel = t.teams == 2 ? int4_tile_kernel<T, 2> : int4_tile_kernel<T, 1>;
+  auto kernel = t.team_warps == 8 ? int4_tile_kernel<T, 8> : int4_tile_kernel<T, 4>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(226 * 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(t.grid);
-  cfg.blockDim = dim3(threads_of(t.teams));
+  cfg.blockDim = dim3(threads_of(t.team_warps));
   cfg.dynamicSmemBytes = t.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
