@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "int8mm.h"
+#include "ptx.cuh"
 
 namespace i8mm {
 
@@ -63,6 +64,21 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// ---------------------------------------------------------------- waits
+//
+// mbar_wait_bounded (ptx.cuh) for a role that waits long and has time: it sleeps between its polls,
+// which otherwise take issue slots from the warps it waits for.
+__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            uint32_t ns) {
+#pragma unroll 1
+  for (int i = 0; i < 20000; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    __nanosleep(ns);
+  }
+  return mbar_wait_bounded(bar, parity, abort);
+}
+
 // ---------------------------------------------------------------- 4-bit weights
 //
 // Of the 8 neighbours k = 8j .. 8j+7 in a 32-bit word, nibble i (from the low end) holds
@@ -74,6 +90,13 @@ __host__ __device__ constexpr int int4_order(int i) { return i < 4 ? 2 * i : 2 *
 __host__ __device__ constexpr int int4_nibble(int j) { return (j & 1) * 4 + (j >> 1); }
 
 constexpr int kInt4Zero = 8;  // the zero point where none is given
+
+// (w & mask) | ones in one instruction: left to itself the compiler spends two and more on it.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t ones) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(ones));
+  return r;
+}
 
 // W_hat of 4-bit words: the group's constants, and 8 values of a word.  A nibble set into the low
 // mantissa bits of 1024 (fp16) or 128 (bf16) reads as that number plus the code.
@@ -91,8 +114,9 @@ struct Int4Values<__half> {
   __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
     const __half2 sixteenth = __float2half2_rn(0.0625f);
     const uint32_t w8 = w >> 8;
-    const uint32_t a[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u,
-                           (w8 & 0x000F000Fu) | 0x64006400u, (w8 & 0x00F000F0u) | 0x64006400u};
+    constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, k1024 = 0x64006400u;
+    const uint32_t a[4] = {and_or(w, kLow, k1024), and_or(w, kHigh, k1024), and_or(w8, kLow, k1024),
+                           and_or(w8, kHigh, k1024)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 h = *reinterpret_cast<const __half2*>(&a[i]);
@@ -112,7 +136,7 @@ struct Int4Values<__nv_bfloat16> {
   __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t a = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      const uint32_t a = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
       const __nv_bfloat162 v =
           __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), z0), s);
       out[i] = *reinterpret_cast<const uint32_t*>(&v);

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
       for (int t = t0; ok && t < p.tiles; t += dt) {
         const int m0 = t % p.m_tiles * p.tn, n0 = t / p.m_tiles * kTileN;
         for (int k = k_begin; k < k_end; ++k) {
-          if (!mbar_wait_bounded(&S.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+          if (!wait_asleep(&S.empty[stage], phase ^ 1u, abort, 20)) { ok = false; break; }
           uint8_t* dst = ring + stage * sbytes;
           mbar_arrive_expect_tx(&S.full[stage], static_cast<uint32_t>(sbytes));
           tma_load_2d(&map_w, dst, &S.full[stage], k * (kStepK / 2), n0);
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     uint32_t d_phase = 0;
     for (int t = t0; t < p.tiles; t += dt) {
       const int m0 = t % p.m_tiles * p.tn, n = t / p.m_tiles * kTileN + quad * 32 + lane;
-      if (!warp_wait(&S.d_full[slot], d_phase, abort)) { ok = false; break; }
+      if (!__all_sync(~0u, wait_asleep(&S.d_full[slot], d_phase, abort, 100))) { ok = false; break; }
       tc_fence_after();
       const bool n_ok = n < p.N;
       const float b = (p.bias && n_ok) ? to_f32(static_cast<const T*>(p.bias)[n]) : 0.0f;
