@@ -104,42 +104,43 @@ template <typename T>
 struct Int4Values;
 template <>
 struct Int4Values<__half> {
-  __half2 s, z0, z1;
+  uint32_t s, z0, z1;
   __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
-    s = *reinterpret_cast<const __half2*>(&s2);
+    s = s2;
     const float zf = static_cast<float>(z);
-    z0 = __float2half2_rn(1024.0f + zf);   // exact up to 2048
-    z1 = __float2half2_rn(-64.0f - zf);    // of a code in bits 4..7: (1024 + 16 u) / 16
+    z0 = pack2<__half>(1024.0f + zf, 1024.0f + zf);  // exact up to 2048
+    z1 = pack2<__half>(-64.0f - zf, -64.0f - zf);    // of a code in bits 4..7: (1024 + 16 u) / 16
   }
   __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-    const uint32_t w8 = w >> 8;
     constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, k1024 = 0x64006400u;
+    constexpr uint32_t kSixteenth = 0x2C002C00u;
+    const uint32_t w8 = w >> 8;
     const uint32_t a[4] = {and_or(w, kLow, k1024), and_or(w, kHigh, k1024), and_or(w8, kLow, k1024),
                            and_or(w8, kHigh, k1024)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __half2 h = *reinterpret_cast<const __half2*>(&a[i]);
-      const __half2 d = (i & 1) ? __hfma2(h, sixteenth, z1) : __hsub2(h, z0);
-      const __half2 v = __hmul2(d, s);
-      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+      uint32_t d;
+      if (i & 1)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a[i]), "r"(kSixteenth), "r"(z1));
+      else
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a[i]), "r"(z0));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(d), "r"(s));
     }
   }
 };
 template <>
 struct Int4Values<__nv_bfloat16> {
-  __nv_bfloat162 s, z0;
+  uint32_t s, z0;
   __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
-    s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-    z0 = __float2bfloat162_rn(128.0f + static_cast<float>(z));
+    s = s2;
+    z0 = pack2<__nv_bfloat16>(128.0f + static_cast<float>(z), 128.0f + static_cast<float>(z));
   }
   __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t a = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
-      const __nv_bfloat162 v =
-          __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), z0), s);
-      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+      uint32_t d;
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(z0));
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(d), "r"(s));
     }
   }
 };

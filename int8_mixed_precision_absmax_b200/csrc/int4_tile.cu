@@ -84,9 +84,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
       : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
   return v;
 }
 
@@ -281,7 +283,8 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     const int g_mul = kStepK / p.group, g_half = first * 32 / p.group;
     const int g_steps = p.group < kStepK ? 1 : p.group / kStepK;
     const bool odd_stages = p.stages % kTeams != 0;
-    int stage = 0, as = 0, turn = 0;  // the teams take steps in turn
+    // the teams take the steps in turn, on from tile to tile; the rings' places of this team's next
+    int stage = team, as = team, skip = team;  // skip: of a tile's steps before it
     uint32_t phase = 0, a_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
       const long long n = min(t / p.m_tiles * kTileN + row, p.N - 1);
@@ -289,22 +292,17 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
       const uint8_t* zrow = p.zeros ? p.zeros + n * p.groups : nullptr;
       GroupChunk cur = {}, nxt = {};
       int held = -1;  // first group of cur
-      // this half of step k: group k g_mul + g_half where a step holds several, otherwise one group
+      int k = k_begin + skip;
+      // this part of step k: group k g_mul + g_half where a step holds several, otherwise one group
       // for every g_steps steps, the next of them in g_left
-      int g_long = k_begin / g_steps, g_left = g_steps - k_begin % g_steps;
-      for (int k = k_begin; k < k_end; ++k) {
+      int g_long = k / g_steps, g_left = g_steps - k % g_steps;
+      for (; k < k_end; k += kTeams) {
         const int s_now = stage, a_now = as;
         const uint32_t ph_now = phase, a_ph_now = a_phase;
-        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-        if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
+        if ((stage += kTeams) >= p.stages) { stage -= p.stages; phase ^= 1u; }
+        if ((as += kTeams) >= p.a_stages) { as -= p.a_stages; a_phase ^= 1u; }
         const int g = p.group < kStepK ? k * g_mul + g_half : g_long;
-        if (--g_left == 0) {
-          g_left = g_steps;
-          ++g_long;
-        }
-        const bool mine = turn == team;
-        if (++turn == kTeams) turn = 0;
-        if (!mine) continue;
+        for (g_left -= kTeams; g_left <= 0; g_left += g_steps) ++g_long;
         const int chunk = g & ~7;
         if (chunk != held) {
           if (chunk == held + 8 && held >= 0) cur = nxt;
@@ -343,6 +341,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.a_full[a_now]);
       }
+      skip = k - k_end;
     }
     if (!ok) report(p.status);
   } else {
@@ -412,16 +411,35 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     cluster_barrier_sync();
     if (!S.abort) {
       const int m0 = t0 % p.m_tiles * p.tn, n0 = t0 / p.m_tiles * kTileN;
+      // 4 channels of a token at a time
       const int c_begin = p.tn * split / p.splits, c_end = p.tn * (split + 1) / p.splits;
-      const uint32_t base = smem_addr(ring);
-      for (int i = c_begin * kTileN + static_cast<int>(threadIdx.x); i < c_end * kTileN; i += threads_of(TW)) {
-        const long long m = m0 + i / kTileN;
-        const int n = n0 + i % kTileN;
+      constexpr int kRow = kTileN / 4;
+      uint32_t base[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) base[r] = r < p.splits ? mapa_shared(smem_addr(ring), r) : 0;
+      for (int i = c_begin * kRow + static_cast<int>(threadIdx.x); i < c_end * kRow; i += threads_of(TW)) {
+        const long long m = m0 + i / kRow;
+        const int n = n0 + i % kRow * 4;
         if (m >= p.M || n >= p.N) continue;
-        float v = 0.0f;
-        for (int r = 0; r < p.splits; ++r) v += ld_cluster_f32(mapa_shared(base, r) + 4u * i);
-        if (p.bias) v += to_f32(static_cast<const T*>(p.bias)[n]);
-        static_cast<T*>(p.Y)[m * p.N + n] = from_f32<T>(v);
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < p.splits) v[r] = ld_cluster_f32x4(base[r] + 16u * i);
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+          if (r < p.splits) {
+            v[0].x += v[r].x;
+            v[0].y += v[r].y;
+            v[0].z += v[r].z;
+            v[0].w += v[r].w;
+          }
+        }
+        const float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        T* y = static_cast<T*>(p.Y) + m * p.N + n;
+        const T* bias = static_cast<const T*>(p.bias) + n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < p.N) y[e] = from_f32<T>(f[e] + (p.bias ? to_f32(bias[e]) : 0.0f));
       }
     }
     __syncwarp();
