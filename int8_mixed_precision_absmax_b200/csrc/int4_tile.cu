@@ -8,11 +8,11 @@
 // tensor core's operand type) and store it to tensor memory, from where tcgen05.mma takes its A
 // operand; X comes through TMA as the B operand.  Sums are float32 in tensor memory.
 //
-// Roles (448 threads): warps 0-7 dequantize (two for each quadrant of 32 tensor-memory lanes, each
-// 64 of a step's 128 k), warps 8-11 are the epilogue, warp 12 issues TMA, warp 13 allocates tensor
-// memory and issues the MMAs.  Rings: `stages` steps of codes and X in shared memory, `a_stages`
-// steps of W_hat and `d_slots` accumulators in tensor memory (two where they fit: the epilogue of
-// a tile overlaps the next tile's main loop).
+// Roles: two teams of warps dequantize the steps of 128 k in turn and, after a tile's last, store its
+// results; one warp issues TMA, one allocates tensor memory and issues the MMAs.  (Warps of their own
+// for the results cost the dequantizing ones registers, whose lack made a third of their
+// instructions moves of constants.)  Rings: `stages` steps of codes and X in shared memory,
+// `a_stages` steps of W_hat in tensor memory.
 //
 // Few tiles: the K axis is split over the CTAs of a cluster, which leave their partial sums in
 // shared memory; each CTA then adds up a slice of the tokens from all of them, in rank order.
@@ -32,8 +32,8 @@ namespace {
 constexpr int kTileN = 128;   // channels per tile
 constexpr int kStepK = 128;   // k per step
 constexpr int kCodeBytes = kTileN * kStepK / 2;
-constexpr int kTeams = 2, kEpiWarps = 4;  // teams of warps that dequantize the steps in turn
-__host__ __device__ constexpr int threads_of(int team_warps) { return (kTeams * team_warps + kEpiWarps + 2) * 32; }
+constexpr int kTeams = 2;
+__host__ __device__ constexpr int threads_of(int team_warps) { return (kTeams * team_warps + 2) * 32; }
 constexpr int kMaxStages = 10, kMaxA = 4;
 constexpr int kACols = kStepK / 2;  // tensor-memory columns of a step of W_hat
 
@@ -44,22 +44,22 @@ struct TileArgs {
   void* Y;
   int32_t* status;
   int M, N, K, group, groups;
-  int tn, stages, a_stages, d_slots, tmem_cols, splits;
+  int tn, stages, a_stages, tmem_cols, splits;
   int m_tiles, tiles, steps;
 };
 
 struct TileShared {  // behind the ring
-  uint4 turn[kEpiWarps][16 * 32 * 2 / 16];
+  uint4 turn[kTeams * 8][8 * 32 * 2 / 16];  // of each dequantizing warp: 8 tokens x 32 channels
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t a_full[kMaxA], a_empty[kMaxA];
-  uint64_t d_full[2], d_empty[2];
+  uint64_t d_full, d_empty;
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
-// tensor-memory columns from one accumulator to the next
-__host__ __device__ constexpr int slot_cols(int tn) { return (tn + 31) / 32 * 32; }
+// tensor-memory columns of the accumulator
+__host__ __device__ constexpr int acc_cols(int tn) { return (tn + 31) / 32 * 32; }
 __host__ __device__ constexpr int stage_bytes(int tn) { return kCodeBytes + tn * kStepK * 2; }
 
 // One lane of a converged warp, the same each time.  Where the rest of a step's code is the whole
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
   const int sbytes = stage_bytes(p.tn);
   TileShared& S = *reinterpret_cast<TileShared*>(ring + p.stages * sbytes);
   constexpr int kDequantWarps = kTeams * TW;
-  constexpr int kTmaWarp = kDequantWarps + kEpiWarps, kMmaWarp = kTmaWarp + 1;
+  constexpr int kTmaWarp = kDequantWarps, kMmaWarp = kTmaWarp + 1;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -181,10 +181,8 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
       mbar_init(&S.a_full[s], TW);
       mbar_init(&S.a_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&S.d_full[s], 1);
-      mbar_init(&S.d_empty[s], kEpiWarps);
-    }
+    mbar_init(&S.d_full, 1);
+    mbar_init(&S.d_empty, kDequantWarps);
     mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbarrier_init();
@@ -204,7 +202,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
   grid_launch_dependents();
 
   const uint32_t tmem = S.tmem_base;
-  const uint32_t a_base = tmem + static_cast<uint32_t>(p.d_slots * slot_cols(p.tn));
+  const uint32_t a_base = tmem + static_cast<uint32_t>(acc_cols(p.tn));
   volatile int* abort = &S.abort;
   // tiles t0, t0 + dt, ...; this CTA's part of the steps of each
   const int split = p.splits > 1 ? static_cast<int>(blockIdx.x) % p.splits : 0;
@@ -239,12 +237,12 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     const uint32_t idesc = tile_idesc<T>(p.tn);
     const uint64_t b0 = sw128_kmajor_desc(smem_addr(ring + kCodeBytes));  // of stage 0; in 16 bytes:
     const uint32_t b_stage = static_cast<uint32_t>(sbytes) >> 4, b_half = static_cast<uint32_t>(p.tn) * 8;
-    int stage = 0, as = 0, slot = 0;
+    int stage = 0, as = 0;
     uint32_t phase = 0, a_phase = 0, d_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
-      if (!warp_wait(&S.d_empty[slot], d_phase ^ 1u, abort)) { ok = false; break; }
+      if (!warp_wait(&S.d_empty, d_phase ^ 1u, abort)) { ok = false; break; }
+      d_phase ^= 1u;
       tc_fence_after();
-      const uint32_t d = tmem + static_cast<uint32_t>(slot * slot_cols(p.tn));
       for (int k = k_begin; k < k_end; ++k) {
         if (!warp_wait(&S.full[stage], phase, abort) || !warp_wait(&S.a_full[as], a_phase, abort)) {
           ok = false;
@@ -256,7 +254,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kStepK / 16; ++j)
-            mma_ts(d, a + 8u * j, b + (j / 4) * b_half + (j % 4) * 2, idesc, k > k_begin || j > 0);
+            mma_ts(tmem, a + 8u * j, b + (j / 4) * b_half + (j % 4) * 2, idesc, k > k_begin || j > 0);
           mma_commit(&S.empty[stage]);
           mma_commit(&S.a_empty[as]);
         }
@@ -265,9 +263,8 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
         if (++as == p.a_stages) { as = 0; a_phase ^= 1u; }
       }
       if (!ok) break;
-      if (elect_one()) mma_commit(&S.d_full[slot]);
+      if (elect_one()) mma_commit(&S.d_full);
       __syncwarp();
-      if (++slot == p.d_slots) { slot = 0; d_phase ^= 1u; }
     }
     if (elect_one()) mma_commit(&S.drain);  // every MMA is done before tensor memory is freed
     __syncwarp();
@@ -285,7 +282,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     const bool odd_stages = p.stages % kTeams != 0;
     // the teams take the steps in turn, on from tile to tile; the rings' places of this team's next
     int stage = team, as = team, skip = team;  // skip: of a tile's steps before it
-    uint32_t phase = 0, a_phase = 0;
+    uint32_t phase = 0, a_phase = 0, d_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
       const long long n = min(t / p.m_tiles * kTileN + row, p.N - 1);
       const T* srow = static_cast<const T*>(p.scales) + n * p.groups;
@@ -341,60 +338,53 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.a_full[a_now]);
       }
+      if (!ok) break;
       skip = k - k_end;
-    }
-    if (!ok) report(p.status);
-  } else {
-    const int quad = warp & 3;
-    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    int slot = 0;
-    uint32_t d_phase = 0;
-    for (int t = t0; t < p.tiles; t += dt) {
-      const int m0 = t % p.m_tiles * p.tn, n = t / p.m_tiles * kTileN + quad * 32 + lane;
-      if (!__all_sync(~0u, wait_asleep(&S.d_full[slot], d_phase, abort, 100))) { ok = false; break; }
+
+      // The tile's results: this warp's 32 channels, every (warps / 4)th 16 of the tokens.
+      if (!__all_sync(~0u, wait_asleep(&S.d_full, d_phase, abort, 20))) { ok = false; break; }
+      d_phase ^= 1u;
       tc_fence_after();
-      const bool n_ok = n < p.N;
-      const float b = (p.bias && n_ok) ? to_f32(static_cast<const T*>(p.bias)[n]) : 0.0f;
+      const int m0 = t % p.m_tiles * p.tn, n_lane = t / p.m_tiles * kTileN + row;
+      const bool n_ok = n_lane < p.N, vectors = p.N % 8 == 0;
+      const float b = (p.bias && n_ok) ? to_f32(static_cast<const T*>(p.bias)[n_lane]) : 0.0f;
       float* part = reinterpret_cast<float*>(ring);  // splits > 1: the ring is drained
       T* Y = static_cast<T*>(p.Y);
-      T* turned = reinterpret_cast<T*>(S.turn[quad]);  // 16 tokens x the warp's 32 channels
-      const bool vectors = p.N % 8 == 0;
-      const uint32_t d = tmem + static_cast<uint32_t>(slot * slot_cols(p.tn)) + lane_base;
-      for (int c = 0; c < p.tn; c += 16) {
+      T* turned = reinterpret_cast<T*>(S.turn[warp]);
+      for (int c = warp / 4 * 16; c < p.tn; c += kDequantWarps / 4 * 16) {
         uint32_t r[16];
         __syncwarp();
-        tmem_ld16(d + static_cast<uint32_t>(c), r);
+        tmem_ld16(tmem + static_cast<uint32_t>(c) + lane_base, r);
         tmem_ld_wait();
         if (p.splits > 1) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            part[(c + j) * kTileN + quad * 32 + lane] = __uint_as_float(r[j]);
+          for (int j = 0; j < 16; ++j) part[(c + j) * kTileN + row] = __uint_as_float(r[j]);
         } else if (vectors) {
           // a lane has one channel of 16 tokens: through shared memory to 8 channels of one token
 #pragma unroll
-          for (int j = 0; j < 16; ++j) turned[j * 32 + lane] = from_f32<T>(__uint_as_float(r[j]) + b);
-          __syncwarp();
-#pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int j = lane / 4 + 8 * i;
-            const long long m = m0 + c + j;
-            const int n8 = n - lane + lane % 4 * 8;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              turned[j * 32 + lane] = from_f32<T>(__uint_as_float(r[8 * i + j]) + b);
+            __syncwarp();
+            const long long m = m0 + c + 8 * i + lane / 4;
+            const int n8 = n_lane - lane + lane % 4 * 8;
             if (m < p.M && n8 < p.N)
               *reinterpret_cast<uint4*>(Y + m * p.N + n8) =
-                  *reinterpret_cast<const uint4*>(turned + j * 32 + lane % 4 * 8);
+                  *reinterpret_cast<const uint4*>(turned + lane / 4 * 32 + lane % 4 * 8);
           }
         } else if (n_ok) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const long long m = m0 + c + j;
-            if (m < p.M) Y[m * p.N + n] = from_f32<T>(__uint_as_float(r[j]) + b);
+            if (m < p.M) Y[m * p.N + n_lane] = from_f32<T>(__uint_as_float(r[j]) + b);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.d_empty[slot]);
-      if (++slot == p.d_slots) { slot = 0; d_phase ^= 1u; }
+      if (lane == 0) mbar_arrive(&S.d_empty);
     }
     if (!ok) report(p.status);
   }
@@ -450,7 +440,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
 namespace {
 
 struct TilePlan {
-  int tn, stages, a_stages, d_slots, tmem_cols, splits, team_warps, grid;
+  int tn, stages, a_stages, tmem_cols, splits, team_warps, grid;
   size_t smem;
 };
 
@@ -484,8 +474,7 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
   }
   t.tmem_cols = per_sm == 2 ? 256 : 512;
   t.team_warps = per_sm == 2 ? 4 : 8;
-  t.d_slots = (t.splits == 1 && 2 * slot_cols(t.tn) + 2 * kACols <= t.tmem_cols) ? 2 : 1;
-  t.a_stages = (t.tmem_cols - t.d_slots * slot_cols(t.tn)) / kACols;
+  t.a_stages = (t.tmem_cols - acc_cols(t.tn)) / kACols;
   if (t.a_stages > kMaxA) t.a_stages = kMaxA;
   const size_t budget = (per_sm == 2 ? 113 : 226) * 1024 - 1024 - sizeof(TileShared);
   t.stages = static_cast<int>(budget / stage_bytes(t.tn));
@@ -522,7 +511,6 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   p.tn = t.tn;
   p.stages = t.stages;
   p.a_stages = t.a_stages;
-  p.d_slots = t.d_slots;
   p.tmem_cols = t.tmem_cols;
   p.splits = t.splits;
   p.m_tiles = (a.M + t.tn - 1) / t.tn;
