@@ -105,11 +105,11 @@ struct Int4Values;
 template <>
 struct Int4Values<__half> {
   uint32_t s, z0, z1;
+  // the scale in both halves, and the zero point (below 64)
   __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
     s = s2;
-    const float zf = static_cast<float>(z);
-    z0 = pack2<__half>(1024.0f + zf, 1024.0f + zf);  // exact up to 2048
-    z1 = pack2<__half>(-64.0f - zf, -64.0f - zf);    // of a code in bits 4..7: (1024 + 16 u) / 16
+    z0 = 0x64006400u + z * 0x00010001u;  // 1024 + z
+    z1 = 0xD400D400u + z * 0x00100010u;  // -64 - z, of a code in bits 4..7: (1024 + 16 u) / 16
   }
   __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
     constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, k1024 = 0x64006400u;
@@ -133,7 +133,7 @@ struct Int4Values<__nv_bfloat16> {
   uint32_t s, z0;
   __device__ __forceinline__ void set(uint32_t s2, uint32_t z) {
     s = s2;
-    z0 = pack2<__nv_bfloat16>(128.0f + static_cast<float>(z), 128.0f + static_cast<float>(z));
+    z0 = 0x43004300u + z * 0x00010001u;  // 128 + z
   }
   __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
 #pragma unroll

@@ -102,50 +102,47 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(~0u, mbar_wait_bounded(bar, parity, abort));
 }
 
-// 8 consecutive groups' scales and zero points of a row, from group g0 (a multiple of 8) on.  Groups
-// past the row's end repeat the last one (they meet zero activations only).
-struct GroupChunk {
-  uint32_t s[4], z[2];
+// The scales and zero points of NG consecutive groups of a row, from group g (a multiple of NG) on.
+// Groups past the row's end repeat the last one (they meet zero activations only).
+template <int NG>
+struct RowGroups {
+  uint32_t s[(NG + 1) / 2], z;  // two scales, four zero points to a word
+  __device__ __forceinline__ uint32_t scale2(int i) const {  // in both halves
+    return __byte_perm(s[i / 2], s[i / 2], (i & 1) ? 0x3232 : 0x1010);
+  }
+  template <bool ZP>
+  __device__ __forceinline__ uint32_t zero(int i) const {
+    return ZP ? z >> (8 * i) & 0xFFu : static_cast<uint32_t>(kInt4Zero);
+  }
 };
-template <typename T>
-__device__ __forceinline__ void load_chunk(GroupChunk& c, const T* scales, const uint8_t* zeros,
-                                           int g0, int groups) {
-  const uint16_t* s16 = reinterpret_cast<const uint16_t*>(scales);
-  if (g0 >= groups) return;  // a prefetch past the end
-  if ((groups & 7) == 0) {
-    const uint4 v = *reinterpret_cast<const uint4*>(s16 + g0);
-    c.s[0] = v.x, c.s[1] = v.y, c.s[2] = v.z, c.s[3] = v.w;
-    if (zeros) {
-      const uint2 w = *reinterpret_cast<const uint2*>(zeros + g0);
-      c.z[0] = w.x, c.z[1] = w.y;
+template <int NG, bool ZP>
+__device__ __forceinline__ void load_groups(RowGroups<NG>& r, const uint16_t* s, const uint8_t* z, int g,
+                                            int groups) {
+  if constexpr (NG == 1) {
+    g = min(g, groups - 1);
+    r.s[0] = s[g];
+    r.z = ZP ? z[g] : 0;
+  } else {
+    if (groups % NG == 0) {  // every row starts on a whole vector
+      g = min(g, groups - NG);
+      if constexpr (NG == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(s + g);
+        r.s[0] = v.x, r.s[1] = v.y;
+        if (ZP) r.z = *reinterpret_cast<const uint32_t*>(z + g);
+      } else {
+        r.s[0] = *reinterpret_cast<const uint32_t*>(s + g);
+        if (ZP) r.z = *reinterpret_cast<const uint16_t*>(z + g);
+      }
+      return;
     }
-    return;
-  }
+    r.s[0] = r.s[NG / 4] = r.z = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int g = g0 + 2 * i;
-    if ((groups & 1) == 0 && g < groups) {
-      c.s[i] = *reinterpret_cast<const uint32_t*>(s16 + g);
-    } else {
-      c.s[i] = s16[min(g, groups - 1)] | static_cast<uint32_t>(s16[min(g + 1, groups - 1)]) << 16;
-    }
-  }
-  if (zeros) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c.z[i] = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        c.z[i] |= static_cast<uint32_t>(zeros[min(g0 + 4 * i + e, groups - 1)]) << (8 * e);
+    for (int i = 0; i < NG; ++i) {
+      const int at = min(g + i, groups - 1);
+      r.s[i / 2] |= static_cast<uint32_t>(s[at]) << (16 * (i & 1));
+      if (ZP) r.z |= static_cast<uint32_t>(z[at]) << (8 * i);
     }
   }
-}
-__device__ __forceinline__ uint32_t chunk_scale2(const GroupChunk& c, int j) {  // in both halves
-  const uint32_t a = (j & 4) ? ((j & 2) ? c.s[3] : c.s[2]) : ((j & 2) ? c.s[1] : c.s[0]);
-  return __byte_perm(a, a, (j & 1) ? 0x3232 : 0x1010);
-}
-__device__ __forceinline__ uint32_t chunk_zero(const GroupChunk& c, int j) {
-  return (((j & 4) ? c.z[1] : c.z[0]) >> (8 * (j & 3))) & 0xFFu;
 }
 
 template <typename T>
@@ -159,7 +156,8 @@ __host__ __device__ constexpr uint32_t tile_idesc(int n) {
 
 // TW warps dequantize a step: 4 where two blocks share an SM, each warp all of a step's k for its 32
 // channels; 8 where a block has the SM to itself, each half of them.
-template <typename T, int TW>
+// GROUP: 32, 64, or 128 for all multiples of 128; ZP: zero points are given.
+template <typename T, int TW, int GROUP, bool ZP>
 __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     int4_tile_kernel(const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const TileArgs p) {
@@ -277,36 +275,34 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);  // of the 64-byte swizzle
-    const int g_mul = kStepK / p.group, g_half = first * 32 / p.group;
-    const int g_steps = p.group < kStepK ? 1 : p.group / kStepK;
+    constexpr int NG = GROUP / 32 < kChunks ? kChunks * 32 / GROUP : 1;  // groups of a warp's part
+    const int g_steps = GROUP == 128 ? p.group / kStepK : 1;
     const bool odd_stages = p.stages % kTeams != 0;
     // the teams take the steps in turn, on from tile to tile; the rings' places of this team's next
     int stage = team, as = team, skip = team;  // skip: of a tile's steps before it
     uint32_t phase = 0, a_phase = 0, d_phase = 0;
     for (int t = t0; ok && t < p.tiles; t += dt) {
       const long long n = min(t / p.m_tiles * kTileN + row, p.N - 1);
-      const T* srow = static_cast<const T*>(p.scales) + n * p.groups;
-      const uint8_t* zrow = p.zeros ? p.zeros + n * p.groups : nullptr;
-      GroupChunk cur = {}, nxt = {};
-      int held = -1;  // first group of cur
+      const uint16_t* srow = static_cast<const uint16_t*>(p.scales) + n * p.groups;
+      const uint8_t* zrow = ZP ? p.zeros + n * p.groups : nullptr;
       int k = k_begin + skip;
-      // this part of step k: group k g_mul + g_half where a step holds several, otherwise one group
-      // for every g_steps steps, the next of them in g_left
-      int g_long = k / g_steps, g_left = g_steps - k % g_steps;
+      // groups of this part of step k; long ones last g_steps steps, g_left more from step k on
+      int g = GROUP == 128 ? k / g_steps : k * (kStepK / GROUP) + first * 32 / GROUP;
+      int g_left = g_steps - k % g_steps;
+      RowGroups<NG> next;
+      load_groups<NG, ZP>(next, srow, zrow, g, p.groups);
       for (; k < k_end; k += kTeams) {
         const int s_now = stage, a_now = as;
         const uint32_t ph_now = phase, a_ph_now = a_phase;
         if ((stage += kTeams) >= p.stages) { stage -= p.stages; phase ^= 1u; }
         if ((as += kTeams) >= p.a_stages) { as -= p.a_stages; a_phase ^= 1u; }
-        const int g = p.group < kStepK ? k * g_mul + g_half : g_long;
-        for (g_left -= kTeams; g_left <= 0; g_left += g_steps) ++g_long;
-        const int chunk = g & ~7;
-        if (chunk != held) {
-          if (chunk == held + 8 && held >= 0) cur = nxt;
-          else load_chunk<T>(cur, srow, zrow, chunk, p.groups);
-          held = chunk;
-          load_chunk<T>(nxt, srow, zrow, chunk + 8, p.groups);
+        const RowGroups<NG> now = next;
+        if (GROUP == 128) {
+          for (g_left -= kTeams; g_left <= 0; g_left += g_steps) ++g;
+        } else {
+          g += kTeams * (kStepK / GROUP);
         }
+        if (k + kTeams < k_end) load_groups<NG, ZP>(next, srow, zrow, g, p.groups);
         // Where the stage's last step was the other team's: only once that has been multiplied is the
         // barrier's phase the one before this step's.
         if (odd_stages && !warp_wait(&S.empty[s_now], ph_now ^ 1u, abort)) { ok = false; break; }
@@ -316,10 +312,7 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
         Int4Values<T> q;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          // a new group for every chunk of 32, every second one, or none within the step's part
-          const int gc = (g & 7) + (p.group == 32 ? c : p.group == 64 ? c / 2 : 0);
-          if (c == 0 || p.group == 32 || (p.group == 64 && c == 2))
-            q.set(chunk_scale2(cur, gc), zrow ? chunk_zero(cur, gc) : kInt4Zero);
+          if (c * 32 % GROUP == 0) q.set(now.scale2(c * 32 / GROUP), now.template zero<ZP>(c * 32 / GROUP));
           const uint4 w = *reinterpret_cast<const uint4*>(codes + row * 64 + ((first + c) ^ swz) * 16);
           uint32_t out[16];
           q.word(w.x, out);
@@ -485,6 +478,18 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
   return t;
 }
 
+template <typename T, int TW, bool ZP>
+auto kernel_of_group(int group) {
+  return group == 32 ? int4_tile_kernel<T, TW, 32, ZP>
+                     : group == 64 ? int4_tile_kernel<T, TW, 64, ZP> : int4_tile_kernel<T, TW, 128, ZP>;
+}
+template <typename T>
+auto kernel_of(int team_warps, int group, bool zeros) {
+  if (team_warps == 8)
+    return zeros ? kernel_of_group<T, 8, true>(group) : kernel_of_group<T, 8, false>(group);
+  return zeros ? kernel_of_group<T, 4, true>(group) : kernel_of_group<T, 4, false>(group);
+}
+
 template <typename T>
 cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
   const Int4Weight& w = a.w;
@@ -518,7 +523,7 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
   p.steps = (w.K + kStepK - 1) / kStepK;
-  auto kernel = t.team_warps == 8 ? int4_tile_kernel<T, 8> : int4_tile_kernel<T, 4>;
+  auto kernel = kernel_of<T>(t.team_warps, w.group, w.zeros != nullptr);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(226 * 1024));
   if (e != cudaSuccess) return e;
