@@ -118,6 +118,27 @@ def test_fused_is_the_two_calls(T, R):
         assert torch.equal(h, i8.int8_block_norm(y2, nw, h=torch.empty_like(f)))
 
 
+@pytest.mark.parametrize("T,R", TYPES)
+@pytest.mark.parametrize("M,D", [(700, 64), (616, 1040), (1200, 4096), (600, 12288)])
+def test_usual_calls_of_many_rows(T, R, M, D):
+    """Root-mean-square norms with weights, layer norms with weights and biases, every result wanted:
+    with and without the output norm and the gate."""
+    f = rand(M, D, T=T, seed=D, std=3.0, mean=-0.25)
+    x = rand(M, D, T=R, seed=D + 1, std=2.0)
+    w, pw, nw = (rand(D, T=T, seed=s, mean=1.0) for s in (3, 4, 5))
+    for layer_norm in (False, True):
+        pb, nb = (rand(D, T=T, seed=s) if layer_norm else None for s in (6, 7))
+        check_norm(i8.int8_block_norm(x, w, pb, 1e-5, layer_norm, h=torch.empty_like(f)), x, w, pb,
+                   1e-5, layer_norm)
+        for post in (False, True):
+            for gate in (None, rand(4, D, T=T, seed=8)):
+                y, h = i8.int8_block_residual(f, x, post, pw if post else None, pb if post else None,
+                                              gate, 1.0, 0.25, True, nw, nb, 1e-6, layer_norm)
+                check_sum(y, f, x, post, pw if post else None, pb if post else None, gate, 1.0, 0.25,
+                          1e-6, layer_norm)
+                check_norm(h, y, nw, nb, 1e-6, layer_norm)
+
+
 def test_gate_rows():
     """One gate row for each sequence of a batch: the rows of its tokens."""
     B, S, D = 3, 7, 320
