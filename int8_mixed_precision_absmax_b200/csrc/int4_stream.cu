@@ -32,8 +32,8 @@
 // operands agree: lane t of a quad takes neighbouring words of its row.
 //
 // A block owns a range of 16-row units and takes them in pairs; its warps share the K axis in
-// chunks of 256 columns, each warp with a ring of its own that TMA fills (boxes of 16 rows x 128
-// bytes, 128-byte swizzle).  The first chunks are requested before the wait for the previous
+// chunks of 256 columns, each warp with a ring of its own that TMA fills (boxes of 16 or 32 rows x
+// 128 bytes, 128-byte swizzle).  The first chunks are requested before the wait for the previous
 // launch.  The warp that takes a chunk of the first pair brings that chunk's activations into shared
 // memory for all pairs, so nothing waits for the whole of X.  Partial sums meet in shared memory
 // every `batch` pairs, in an order that does not change.
@@ -345,7 +345,8 @@ __device__ __forceinline__ void digits4(const float (&f)[4], float f1, float f2,
 
 template <typename T, int SUB, bool ZP, bool DIGITS>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
-    int4_stream_kernel(const __grid_constant__ CUtensorMap map_w, const StreamArgs p) {
+    int4_stream_kernel(const __grid_constant__ CUtensorMap map_unit,
+                       const __grid_constant__ CUtensorMap map_pair, const StreamArgs p) {
   extern __shared__ uint8_t stream_smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(stream_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       for (int s = 0; s < p.stages; ++s) mbar_init(&S.full[w][s], 1);
     mbar_init(&S.x_full, 1);
     S.abort = 0;
-    prefetch_tmap(&map_w);
+    prefetch_tmap(&map_unit);
+    prefetch_tmap(&map_pair);
   }
   for (int i = threadIdx.x; i < p.chunks; i += blockDim.x) mbar_init(&S.x_ready[i], 1);
   fence_mbarrier_init();
@@ -393,10 +395,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       const bool two = u + 1 < u1;
       uint8_t* dst = my_ring + f_stage * kStageBytes;
       mbar_arrive_expect_tx(&my_full[f_stage], two ? kStageBytes : kUnitBytes);
-      tma_load_2d(&map_w, dst, &my_full[f_stage], fc * (kChunkK / 2), u * kUnitRows);
-      if (two)
-        tma_load_2d(&map_w, dst + kUnitBytes, &my_full[f_stage], fc * (kChunkK / 2),
-                    (u + 1) * kUnitRows);
+      tma_load_2d(two ? &map_pair : &map_unit, dst, &my_full[f_stage], fc * (kChunkK / 2),
+                  u * kUnitRows);
     }
     ++issued;
     if (++f_stage == p.stages) f_stage = 0;
@@ -491,16 +491,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         } else {
           if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
           const int i = c * 32 + lane;
-          for (int m = 0; m < p.M; ++m) {
-            uint32_t* v = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(m) * p.xstride) + 4 * i;
-            if (i >= pieces) {  // zeros up to the chunk's end
-              *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
-            } else if (std::is_same<T, __half>::value) {
-              // The two operand words of an MMA are a register pair: the words 0 and 2 of 16 bytes
-              // (the low nibbles' columns), then 1 and 3.
-              const uint32_t one = v[1], two = v[2];
-              v[1] = two;
-              v[2] = one;
+          // The two operand words of an MMA are a register pair: of fp16 the words 0 and 2 of 16 bytes
+          // (the low nibbles' columns), then 1 and 3.  Zeros up to the chunk's end.
+          if (std::is_same<T, __half>::value || i >= pieces) {
+#pragma unroll 4
+            for (int m = 0; m < p.M; ++m) {
+              uint4* at = reinterpret_cast<uint4*>(xs + static_cast<size_t>(m) * p.xstride) + i;
+              const uint4 v = *at;
+              *at = i < pieces ? make_uint4(v.x, v.z, v.y, v.w) : make_uint4(0, 0, 0, 0);
             }
           }
         }
@@ -631,7 +629,7 @@ bool plan_stream(int M, int K, int group, StreamPlan& s) {
 }
 
 template <typename T, int SUB, bool ZP, bool DIGITS>
-cudaError_t launch_variant(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s,
+cudaError_t launch_variant(const CUtensorMap (&map)[2], const StreamArgs& p, const StreamPlan& s,
                            int grid, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(int4_stream_kernel<T, SUB, ZP, DIGITS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -647,11 +645,11 @@ cudaError_t launch_variant(const CUtensorMap& map, const StreamArgs& p, const St
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, int4_stream_kernel<T, SUB, ZP, DIGITS>, map, p);
+  return cudaLaunchKernelEx(&cfg, int4_stream_kernel<T, SUB, ZP, DIGITS>, map[0], map[1], p);
 }
 
 template <typename T, bool ZP, bool DIGITS>
-cudaError_t launch_sub(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s,
+cudaError_t launch_sub(const CUtensorMap (&map)[2], const StreamArgs& p, const StreamPlan& s,
                        int grid, cudaStream_t stream) {
   switch (sub_of(p.group)) {
     case 1: return launch_variant<T, 1, ZP, DIGITS>(map, p, s, grid, stream);
@@ -661,7 +659,7 @@ cudaError_t launch_sub(const CUtensorMap& map, const StreamArgs& p, const Stream
 }
 
 template <typename T>
-cudaError_t launch_typed(const CUtensorMap& map, const StreamArgs& p, const StreamPlan& s,
+cudaError_t launch_typed(const CUtensorMap (&map)[2], const StreamArgs& p, const StreamPlan& s,
                          int grid, cudaStream_t stream) {
   if (p.M <= 2)
     return p.zeros ? launch_sub<T, true, true>(map, p, s, grid, stream)
@@ -680,10 +678,12 @@ bool int4_stream_fits(int M, int K, int group) {
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
   const Int4Weight& w = a.w;
   StreamPlan s;
-  CUtensorMap map;
+  CUtensorMap map[2];  // boxes of a unit and of a pair
   if (!plan_stream(a.M, w.K, w.group, s) ||
-      !encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K / 2, w.N, w.K / 2,
-                      kChunkK / 2, kUnitRows))
+      !encode_tmap_2d(&map[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K / 2, w.N, w.K / 2,
+                      kChunkK / 2, kUnitRows) ||
+      !encode_tmap_2d(&map[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K / 2, w.N, w.K / 2,
+                      kChunkK / 2, 2 * kUnitRows))
     return cudaErrorInvalidValue;
   StreamArgs p;
   p.X = a.X;
