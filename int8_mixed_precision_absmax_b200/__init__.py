@@ -503,12 +503,12 @@ def _matrix(t: torch.Tensor, dtypes: tuple, name: str) -> int:
     return t.get_device()
 
 
-def _new(shape, dtype, device: int, stream) -> torch.Tensor:
-    """An output tensor whose memory belongs to the stream that the call runs on."""
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """An output tensor on like's device whose memory belongs to the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _call(what: str, device: int, stream, *args) -> None:
@@ -544,11 +544,11 @@ def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = 
     if symmetric and zeros is not None:
         raise ValueError("zeros is an output of the asymmetric quantizer: pass symmetric=False")
     if codes is None:
-        codes = _new((N, K // 2), torch.uint8, dev, stream)
+        codes = _new(W, (N, K // 2), torch.uint8, stream)
     if scales is None:
-        scales = _new(shape, T, dev, stream)
+        scales = _new(W, shape, T, stream)
     if zeros is None and not symmetric:
-        zeros = _new(shape, torch.uint8, dev, stream)
+        zeros = _new(W, shape, torch.uint8, stream)
     _call("int4_quant_weight", dev, stream, W.data_ptr(), N, K, group_size, T is torch.bfloat16,
           _at(codes, torch.uint8, (N, K // 2), dev, "codes"), _at(scales, T, shape, dev, "scales"),
           None if symmetric else _at(zeros, torch.uint8, shape, dev, "zeros"))
@@ -567,7 +567,7 @@ def int4_dequant_weight(codes: torch.Tensor, scales: torch.Tensor,
         raise TypeError(f"scales must be torch.float16 or torch.bfloat16, got {T}")
     shape = (N, _int4_shapes(K, group_size))
     if W_hat is None:
-        W_hat = _new((N, K), T, dev, stream)
+        W_hat = _new(codes, (N, K), T, stream)
     _call("int4_dequant_weight", dev, stream, codes.data_ptr(),
           _at(scales, T, shape, dev, "scales"),
           None if zeros is None else _at(zeros, torch.uint8, shape, dev, "zeros"), N, K,
@@ -587,7 +587,7 @@ def int4_linear_forward(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     N = codes.shape[0]
     shape = (N, _int4_shapes(K, group_size))
     if Y is None:
-        Y = _new((M, N), T, dev, stream)
+        Y = _new(X, (M, N), T, stream)
     _call("int4_linear_forward", dev, stream, X.data_ptr(), M, K,
           _at(codes, torch.uint8, (N, K // 2), dev, "codes"), _at(scales, T, shape, dev, "scales"),
           None if zeros is None else _at(zeros, torch.uint8, shape, dev, "zeros"),
@@ -612,7 +612,7 @@ def int8_block_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
         if T not in _HALF_TYPES:
             raise TypeError(f"weight and h must be torch.float16 or torch.bfloat16, got {T}")
     if h is None:
-        h = _new((M, D), T, dev, stream)
+        h = _new(x, (M, D), T, stream)
     flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
              | (0 if R is T else _F32_RESIDUAL))
     _call("int8_block_norm", dev, stream, x.data_ptr(), M, D,
@@ -658,9 +658,9 @@ def int8_block_residual(f: torch.Tensor, x: torch.Tensor, post_norm: bool = Fals
         else:
             gate_rows, gate_at = 1, _at(gate, T, vector, dev, "gate")
     if y is None:
-        y = _new(rows, R, dev, stream)
+        y = _new(f, rows, R, stream)
     if h is None and next_norm:
-        h = _new(rows, T, dev, stream)
+        h = _new(f, rows, T, stream)
     flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
              | (0 if R is T else _F32_RESIDUAL) | (_POST_NORM if post_norm else 0))
     _call("int8_block_residual", dev, stream, f.data_ptr(), _at(x, R, rows, dev, "x"), M, D,

@@ -2,6 +2,7 @@
 // what their entry points (api_block.cu) hand to the kernels' launches.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -173,6 +174,21 @@ bool int4_stream_fits(int M, int K, int group);
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
 // more (int4_tile.cu): tcgen05
 cudaError_t launch_int4_tile(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- launches
+
+// Lets `kernel` use `bytes` of dynamic shared memory, once on each device (`done`: of this kernel, a bit
+// for each device).
+inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---------------------------------------------------------------- block norms
 

@@ -631,9 +631,9 @@ bool plan_stream(int M, int K, int group, StreamPlan& s) {
 template <typename T, int SUB, bool ZP, bool DIGITS>
 cudaError_t launch_variant(const CUtensorMap (&map)[2], const StreamArgs& p, const StreamPlan& s,
                            int grid, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(int4_stream_kernel<T, SUB, ZP, DIGITS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmemMost));
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(int4_stream_kernel<T, SUB, ZP, DIGITS>),
+                                   kSmemMost, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -35,6 +35,7 @@ constexpr int kCodeBytes = kTileN * kStepK / 2;
 constexpr int kTeams = 2;
 __host__ __device__ constexpr int threads_of(int team_warps) { return (kTeams * team_warps + 2) * 32; }
 constexpr int kMaxStages = 10, kMaxA = 4;
+constexpr size_t kSmemMost = 226 * 1024;  // of an SM, for one block or for two
 constexpr int kACols = kStepK / 2;  // tensor-memory columns of a step of W_hat
 
 struct TileArgs {
@@ -469,7 +470,7 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
   t.team_warps = per_sm == 2 ? 4 : 8;
   t.a_stages = (t.tmem_cols - acc_cols(t.tn)) / kACols;
   if (t.a_stages > kMaxA) t.a_stages = kMaxA;
-  const size_t budget = (per_sm == 2 ? 113 : 226) * 1024 - 1024 - sizeof(TileShared);
+  const size_t budget = kSmemMost / per_sm - 1024 - sizeof(TileShared);
   t.stages = static_cast<int>(budget / stage_bytes(t.tn));
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   t.smem = static_cast<size_t>(t.stages) * stage_bytes(t.tn) + sizeof(TileShared) + 1024;
@@ -478,16 +479,24 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
   return t;
 }
 
+using TileKernel = void (*)(const CUtensorMap, const CUtensorMap, const TileArgs);
+
+template <typename T, int TW, int GROUP, bool ZP>
+cudaError_t ready(TileKernel& kernel) {
+  static std::atomic<unsigned long long> allowed{0};
+  kernel = int4_tile_kernel<T, TW, GROUP, ZP>;
+  return allow_smem(reinterpret_cast<const void*>(kernel), kSmemMost, allowed);
+}
 template <typename T, int TW, bool ZP>
-auto kernel_of_group(int group) {
-  return group == 32 ? int4_tile_kernel<T, TW, 32, ZP>
-                     : group == 64 ? int4_tile_kernel<T, TW, 64, ZP> : int4_tile_kernel<T, TW, 128, ZP>;
+cudaError_t kernel_of_group(int group, TileKernel& kernel) {
+  return group == 32 ? ready<T, TW, 32, ZP>(kernel)
+                     : group == 64 ? ready<T, TW, 64, ZP>(kernel) : ready<T, TW, 128, ZP>(kernel);
 }
 template <typename T>
-auto kernel_of(int team_warps, int group, bool zeros) {
+cudaError_t kernel_of(int team_warps, int group, bool zeros, TileKernel& kernel) {
   if (team_warps == 8)
-    return zeros ? kernel_of_group<T, 8, true>(group) : kernel_of_group<T, 8, false>(group);
-  return zeros ? kernel_of_group<T, 4, true>(group) : kernel_of_group<T, 4, false>(group);
+    return zeros ? kernel_of_group<T, 8, true>(group, kernel) : kernel_of_group<T, 8, false>(group, kernel);
+  return zeros ? kernel_of_group<T, 4, true>(group, kernel) : kernel_of_group<T, 4, false>(group, kernel);
 }
 
 template <typename T>
@@ -523,9 +532,8 @@ cudaError_t launch_typed(const Int4LinearArgs& a, int num_sms, cudaStream_t stre
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
   p.steps = (w.K + kStepK - 1) / kStepK;
-  auto kernel = kernel_of<T>(t.team_warps, w.group, w.zeros != nullptr);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(226 * 1024));
+  TileKernel kernel = nullptr;
+  const cudaError_t e = kernel_of<T>(t.team_warps, w.group, w.zeros != nullptr, kernel);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(t.grid);
