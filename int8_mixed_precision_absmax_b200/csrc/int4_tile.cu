@@ -474,6 +474,11 @@ TilePlan plan_tile(int M, int N, int K, int num_sms) {
   t.stages = static_cast<int>(budget / stage_bytes(t.tn));
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   t.smem = static_cast<size_t>(t.stages) * stage_bytes(t.tn) + sizeof(TileShared) + 1024;
+  // Where these blocks hold all of an SM's tensor memory, they leave less shared memory than any other
+  // kernel with tensor memory needs (33 KB): none waits on the SM for tensor memory that a cluster here
+  // will not give back before its blocks elsewhere have got theirs.
+  const size_t least = static_cast<size_t>(200 * 1024 / per_sm);
+  if (t.smem < least) t.smem = least;
   t.grid = t.splits > 1 ? static_cast<int>(tiles) * t.splits
                         : static_cast<int>(tiles < capacity ? tiles : capacity);
   return t;

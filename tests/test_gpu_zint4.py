@@ -299,6 +299,47 @@ def test_weights_and_activations_made_just_before():
         W = W.roll(1, 0).contiguous()
 
 
+def test_two_threads_on_two_streams():
+    """Two threads at once, each on a stream of its own, through every kernel of the product: each
+    result is that of the same calls one after the other."""
+    import threading
+
+    Ws = [(torch.randn(512, 1024, device="cuda") * 0.05).half() for _ in range(2)]
+    Xs = [acts(M, 1024, FP16, M) for M in (1, 4, 30, 160)]
+
+    def calls(W):
+        out = []
+        for X in Xs:
+            weight = i8.int4_quant_weight(W, 64, False)
+            Y = i8.int4_linear_forward(X, *weight, group_size=64)
+            out.append((Y, i8.int8_block_norm(Y)))
+        return out
+
+    want = [calls(W) for W in Ws]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            side = torch.cuda.Stream()
+            with torch.cuda.stream(side):
+                for _ in range(30):
+                    got[i] = calls(Ws[i])
+            side.synchronize()
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_offsets_past_32_bits():
     """More than 4 GiB of codes, and more than 4 GiB of outputs."""
     N, K, group = 140000, 65536, 128
