@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads)
   const int words = K / 8;
   SpanWalk at((K + 511) / 512);
   const uint16_t* s16 = reinterpret_cast<const uint16_t*>(scales);
+  grid_dependency_wait();
   uint32_t word[2], scale[2], zero[2];
   auto fetch = [&]() {
 #pragma unroll
@@ -283,11 +284,12 @@ __global__ void __launch_bounds__(kThreads)
         Int4Values<T> q;
         uint32_t r[4];
         q.set(s[i] * 0x10001u, z[i]);
-        q.word(w[i], r);
+        q.template word<false>(w[i], r);
         __stcs(W_hat + row * words + j0 + i * 32, make_uint4(r[0], r[1], r[2], r[3]));
       }
     }
   }
+  grid_launch_dependents();
 }
 
 namespace {
@@ -330,13 +332,23 @@ cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
   const int grid = blocks_for(static_cast<long long>(w.N) * ((w.K + 511) / 512), kWarps, num_sms);
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(w.codes);
   uint4* out = static_cast<uint4*>(W_hat);
-  if (w.bf16)
-    int4_dequant_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(
-        codes, static_cast<const __nv_bfloat16*>(w.scales), w.zeros, w.N, w.K, w.group, w.groups, out);
-  else
-    int4_dequant_kernel<__half><<<grid, kThreads, 0, stream>>>(
-        codes, static_cast<const __half*>(w.scales), w.zeros, w.N, w.K, w.group, w.groups, out);
-  return cudaGetLastError();
+  // launched while the kernel before drains: it waits for that one's results itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const unsigned group = static_cast<unsigned>(w.group);
+  return w.bf16 ? cudaLaunchKernelEx(&cfg, int4_dequant_kernel<__nv_bfloat16>, codes,
+                                     static_cast<const __nv_bfloat16*>(w.scales), w.zeros, w.N, w.K, group,
+                                     w.groups, out)
+                : cudaLaunchKernelEx(&cfg, int4_dequant_kernel<__half>, codes,
+                                     static_cast<const __half*>(w.scales), w.zeros, w.N, w.K, group,
+                                     w.groups, out);
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {

@@ -316,10 +316,10 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
           if (c * 32 % GROUP == 0) q.set(now.scale2(c * 32 / GROUP), now.template zero<ZP>(c * 32 / GROUP));
           const uint4 w = *reinterpret_cast<const uint4*>(codes + row * 64 + ((first + c) ^ swz) * 16);
           uint32_t out[16];
-          q.word(w.x, out);
-          q.word(w.y, out + 4);
-          q.word(w.z, out + 8);
-          q.word(w.w, out + 12);
+          q.template word<true>(w.x, out);
+          q.template word<true>(w.y, out + 4);
+          q.template word<true>(w.z, out + 8);
+          q.template word<true>(w.w, out + 12);
           if (c == 0) {
             if (!warp_wait(&S.a_empty[a_now], a_ph_now ^ 1u, abort)) { ok = false; break; }
             tc_fence_after();
