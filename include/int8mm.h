@@ -371,8 +371,9 @@ int int4_dequant_weight(const uint8_t *codes, const void *scales, const uint8_t 
  * No workspace: calls on different streams do not disturb each other.
  * A NaN or an infinity in a row of X makes the results of that row NaN or infinite (which of the
  * two is not said); so may bfloat16 values of 2^112 and above, whose float32 sums can overflow.
- * With few tokens the products are of the codes themselves; with more (M > 8,
- * or activations beyond one SM's shared memory) of W_hat rounded to T, which has to be finite.
+ * With one or two tokens the products are of the codes themselves, where the activations fit into one
+ * SM's shared memory; up to M = 8, as the sizes decide, of these or of W_hat rounded to T; beyond, of
+ * W_hat rounded to T, which has to be finite.
  * As with int8_linear_forward, the weights may be read before the launch before this one on the
  * stream is done: codes, scales and zeros must not be written by a kernel launched just before
  * that lets its successors start early (int4_quant_weight and ordinary kernels do not).

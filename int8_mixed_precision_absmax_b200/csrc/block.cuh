@@ -179,10 +179,10 @@ cudaError_t launch_int4_quant(const void* W, int N, int K, int group, bool bf16,
 cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
                                 cudaStream_t stream);
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
-// few tokens (int4_stream.cu): up to 8, as long as their activations fit into shared memory
-bool int4_stream_fits(int M, int K, int group);
+// few tokens (int4_stream.cu): up to 8 whose activations fit into shared memory, where it is faster
+bool int4_stream_suits(int M, int N, int K, int group, int num_sms);
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
-// more (int4_tile.cu): tcgen05
+// all others (int4_tile.cu): tcgen05
 cudaError_t launch_int4_tile(const Int4LinearArgs& a, int num_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- launches

@@ -352,8 +352,8 @@ cudaError_t launch_int4_dequant(const Int4Weight& w, void* W_hat, int num_sms,
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
-  return int4_stream_fits(a.M, a.w.K, a.w.group) ? launch_int4_stream(a, num_sms, stream)
-                                      : launch_int4_tile(a, num_sms, stream);
+  return int4_stream_suits(a.M, a.w.N, a.w.K, a.w.group, num_sms) ? launch_int4_stream(a, num_sms, stream)
+                                                                  : launch_int4_tile(a, num_sms, stream);
 }
 
 }  // namespace i8mm

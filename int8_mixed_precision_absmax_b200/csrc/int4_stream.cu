@@ -596,10 +596,16 @@ struct StreamPlan {
 // Columns of 32 SUB are one load of a lane and lie in one group.
 int sub_of(int group) { return group == 32 ? 1 : group == 64 ? 2 : 4; }
 
-// Two blocks of 8 warps on an SM where the activations of all tokens leave room for that, otherwise
-// one of 16 or 8; at least two stages for each warp.  (One token, fp16, groups of 128, us of two
-// blocks of 8 / one of 16 / one of 8: 2368 x 4096 4.0 / 5.5 / 5.1, 16384 x 4096 10.1 / 17.1 / 12.6,
-// 49152 x 12288 57 / 55 / 73; two tokens of 32768 x 8192, where two blocks do not fit, - / 33 / 37.)
+// The block's shape, the first of an order that fits, at least two stages for each warp.  One block of
+// 16 warps brings the activations into shared memory once an SM and lets all warps share the chunks,
+// but with few of them a warp has one in a pair, and waits; two blocks of 8 also fill each other's
+// pauses.  (us of two blocks of 8 / one of 16 / one of 8; K = 4096: one token, N 4096 6.3 / 6.7 / 6.1,
+// N 32768 16.4 / 25.4 / 20.6, 6 tokens, N 4096 - / 7.4 / 6.9; K = 8192: one token, N 4096 9.3 / 8.4 / 8.7,
+// 3 tokens, N 32768 - / 36.7 / 42.0; K = 12288: one token, N 49152 56.3 / 53.5 / 70.0.)
+struct Shape { int warps, per_sm; };
+constexpr Shape kFewChunks[] = {{8, 2}, {8, 1}, {16, 1}}, kManyChunks[] = {{16, 1}, {8, 1}};
+constexpr int kMany = 32;
+
 bool plan_stream(int M, int K, int group, StreamPlan& s) {
   if (M > kMaxTok) return false;
   const bool digits = M <= 2;
@@ -609,8 +615,9 @@ bool plan_stream(int M, int K, int group, StreamPlan& s) {
   // apart: 8, 16 or 32 bytes a lane of digits, twice that in 16 bits
   s.xstride = chunks * kChunkK * (digits ? 1 : 2) +
               (digits ? (sub == 1 ? 32 : sub == 2 ? 64 : 16) : (sub == 1 ? 64 : 16));
-  const struct { int warps, per_sm; } shapes[] = {{8, 2}, {16, 1}, {8, 1}};
-  for (const auto& shape : shapes) {
+  const Shape* shapes = chunks < kMany ? kFewChunks : kManyChunks;
+  for (int i = 0; i < (chunks < kMany ? 3 : 2); ++i) {
+    const Shape& shape = shapes[i];
     s.warps = shape.warps;
     s.per_sm = shape.per_sm;
     const size_t most = shape.per_sm == 2 ? kSmemMost / 2 : kSmemMost;
@@ -670,9 +677,15 @@ cudaError_t launch_typed(const CUtensorMap (&map)[2], const StreamArgs& p, const
 
 }  // namespace
 
-bool int4_stream_fits(int M, int K, int group) {
+// With 4 tokens and more in one block of 8 warps, instructions bound the kernel, and many units to a
+// block are better off with the tensor cores.  (us of this / of int4_tile.cu, N = 4096, 11008, 32768;
+// K = 4096: 6 tokens 6.9 / 8.4, 13.0 / 12.8, 28.4 / 25.9, 8 tokens 7.1 / 8.5, 13.8 / 12.9, 30.6 / 26.1;
+// K = 12288: 4 tokens 13.8 / 13.3, 30.6 / 30.0, 68.3 / 66.8; two tokens 12.3 / 13.2, 26.5 / 29.7,
+// 50.4 / 66.8.)
+bool int4_stream_suits(int M, int N, int K, int group, int num_sms) {
   StreamPlan s;
-  return plan_stream(M, K, group, s);
+  if (!plan_stream(M, K, group, s)) return false;
+  return M < 4 || s.warps * s.per_sm > 8 || N <= 4 * kUnitRows * num_sms;
 }
 
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
