@@ -45,6 +45,7 @@ PAIR_TILES = 2        # int8_linear_forward_ex flag: M > 128 products on CTA pai
 _BFLOAT16, _LAYER_NORM, _F32_RESIDUAL, _POST_NORM = 1, 2, 4, 8
 _HALF_TYPES = (torch.float16, torch.bfloat16)
 _ROW_TYPES = _HALF_TYPES + (torch.float32,)
+_INT_MAX = 0x7FFFFFFF
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libint8mm.so")
 _lib = None
@@ -498,6 +499,8 @@ def _matrix(t: torch.Tensor, dtypes: tuple, name: str) -> int:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions")
+    if max(t.shape) > _INT_MAX:  # the library takes ints
+        raise ValueError(f"{name} has a size of 2^31 or more: {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.get_device()
@@ -525,9 +528,11 @@ def _call(what: str, device: int, stream, *args) -> None:
         raise Int8mmError(status, what)
 
 
-def _int4_shapes(K: int, group_size: int) -> int:
-    """Groups of a row (1 for a group size the library is left to refuse)."""
-    return -(-K // group_size) if group_size > 0 else 1
+def _int4_shapes(N: int, K: int, group_size: int) -> tuple:
+    """The scales' shape (one group a row for a group size the library is left to refuse)."""
+    if N > _INT_MAX or group_size > _INT_MAX:
+        raise ValueError(f"N ({N}) and group_size ({group_size}) must be below 2^31")
+    return (N, -(-K // group_size) if group_size > 0 else 1)
 
 
 def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = True,
@@ -540,7 +545,7 @@ def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = 
     dev = _matrix(W, _HALF_TYPES, "W")
     T = W.dtype
     N, K = W.shape
-    shape = (N, _int4_shapes(K, group_size))
+    shape = _int4_shapes(N, K, group_size)
     if symmetric and zeros is not None:
         raise ValueError("zeros is an output of the asymmetric quantizer: pass symmetric=False")
     if codes is None:
@@ -565,7 +570,7 @@ def int4_dequant_weight(codes: torch.Tensor, scales: torch.Tensor,
     T = scales.dtype
     if T not in _HALF_TYPES:
         raise TypeError(f"scales must be torch.float16 or torch.bfloat16, got {T}")
-    shape = (N, _int4_shapes(K, group_size))
+    shape = _int4_shapes(N, K, group_size)
     if W_hat is None:
         W_hat = _new(codes, (N, K), T, stream)
     _call("int4_dequant_weight", dev, stream, codes.data_ptr(),
@@ -585,7 +590,7 @@ def int4_linear_forward(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     T = X.dtype
     M, K = X.shape
     N = codes.shape[0]
-    shape = (N, _int4_shapes(K, group_size))
+    shape = _int4_shapes(N, K, group_size)
     if Y is None:
         Y = _new(X, (M, N), T, stream)
     _call("int4_linear_forward", dev, stream, X.data_ptr(), M, K,
@@ -694,10 +699,16 @@ class _BlockEnds:
 
     pre_norm: BlockNorm | None = None
     post_norm: BlockNorm | None = None
+    _dtype = torch.float16  # of the product's activations
 
     def _before(self, X: torch.Tensor) -> torch.Tensor:
         X2 = X.reshape(-1, X.shape[-1]).contiguous()
-        return X2 if self.pre_norm is None else self.pre_norm(X2)
+        if self.pre_norm is None:
+            return X2
+        h = None
+        if X2.dtype is torch.float32 and self.pre_norm.weight is None:
+            h = X2.new_empty(X2.shape, dtype=self._dtype)  # nothing else says the layer's type
+        return self.pre_norm(X2, h)
 
     def _after(self, Y: torch.Tensor, residual, gate, x_scale, f_scale, out):
         post = self.post_norm
@@ -798,6 +809,7 @@ class Int4Linear(_BlockEnds):
         weight = weight.contiguous()
         self.codes, self.scales, self.zeros = int4_quant_weight(weight, self.group_size,
                                                                 symmetric)
+        self._dtype = weight.dtype
         self.bias = None if bias is None else bias.to(weight.dtype).contiguous()
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=weight.device)
 

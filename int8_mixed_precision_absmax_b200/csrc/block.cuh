@@ -29,7 +29,6 @@ struct Half2Of<__nv_bfloat16> {
 
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
@@ -38,8 +37,6 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
 // Two neighbours in one 32-bit word, low half first.
 template <typename T>
@@ -83,10 +80,9 @@ __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, vola
 // ---------------------------------------------------------------- 4-bit weights
 //
 // Of the 8 neighbours k = 8j .. 8j+7 in a 32-bit word, nibble i (from the low end) holds
-// k = 8j + kInt4Order(i): 0, 2, 4, 6, 1, 3, 5, 7.  One AND with 0x000F000F (of the word shifted
+// k = 8j + 0, 2, 4, 6, 1, 3, 5, 7.  One AND with 0x000F000F (of the word shifted
 // right by 0, 4, 8, 12) leaves the neighbours (0,1), (2,3), (4,5), (6,7) in the two halves of a
 // register, the order in which a 16-byte load of X holds their factors.
-__host__ __device__ constexpr int int4_order(int i) { return i < 4 ? 2 * i : 2 * i - 7; }
 // The nibble that holds neighbour j of its word.
 __host__ __device__ constexpr int int4_nibble(int j) { return (j & 1) * 4 + (j >> 1); }
 

@@ -335,3 +335,19 @@ def test_layers_without_ends_are_as_before():
     assert Y.shape == (3, 2, 64)
     assert torch.equal(Y.view(6, 64), i8.int8_linear_forward(X.view(6, 128), layer.Wq, layer.w_scale,
                                                              None))
+
+
+@pytest.mark.parametrize("T", [torch.float16, torch.bfloat16])
+def test_layer_of_a_float32_stream_without_norm_weights(T):
+    """The norm's output takes the layer's type where no weight says it."""
+    layer = i8.Int4Linear(rand(64, 128, seed=1, std=0.1).to(T), pre_norm=i8.BlockNorm())
+    x = rand(5, 128, seed=2).float()
+    h = i8.int8_block_norm(x, h=torch.empty(5, 128, dtype=T, device="cuda"))
+    assert torch.equal(layer(x), layer._product(h, None))
+
+
+def test_sizes_past_an_int_are_refused():
+    with pytest.raises(ValueError, match="2\\^31"):
+        i8.int8_block_norm(torch.empty(2 ** 32 + 1, 0, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError, match="2\\^31"):
+        i8.int8_block_norm(torch.empty(0, 2 ** 32 + 16, dtype=torch.float16, device="cuda"))

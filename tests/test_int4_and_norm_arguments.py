@@ -117,3 +117,10 @@ def test_reference_packing_round_trip():
     word = int(codes[0, :4].view("<u4")[0])
     assert [word >> 4 * i & 15 for i in range(8)] == [int(u[0, k]) for k in
                                                       (0, 2, 4, 6, 1, 3, 5, 7)]
+
+
+def test_sizes_past_an_int_are_not_cut_off():
+    assert i8._int4_shapes(8, 100, 64) == (8, 2)
+    for N, group in ((8, 2 ** 32 + 128), (2 ** 32 + 8, 128)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            i8._int4_shapes(N, 256, group)
