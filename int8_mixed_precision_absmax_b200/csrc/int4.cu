@@ -2,7 +2,9 @@
 //
 // Both passes are bound by the bytes of the 16-bit weights (one read or one write, and a quarter of
 // that for the codes).  A lane takes 16 neighbouring columns at a time, so a group's scale is found
-// once for 16 values, and asks for its next ones before it works on those it has.
+// once for 16 values, and asks for its next ones before it works on those it has.  Measured, us, fp16
+// 49152 x 12288, groups of 128: quantizer 276 (5.5 TB/s, 84 % of the measured copy rate), its inverse 269
+// (5.6 TB/s); 4096 x 4096, groups of 64 with zero points: 11.3 and 8.6.
 #include <type_traits>
 
 #include "block.cuh"

@@ -10,7 +10,13 @@
 // weights and gates stay in cache (rows do not allocate in L1).  With many rows a thread takes 4 pieces
 // of 8 elements (blocks small enough that an SM has several rows in flight); with few rows 1, for
 // latency.  A ring of rows copied ahead by each thread was slower (2048 x 12288 after a block: 75 us
-// against 48): it leaves fewer threads, and instructions, about 290 for 8 elements there, bound it.
+// against 48 then): it leaves fewer threads, and instructions were what bound it; packed float32
+// halves the arithmetic.
+//
+// Measured, us: 2048 x 12288 after a block, norm of f, gate of every channel, 41 (4.9 TB/s, 74 % of
+// the measured copy rate; 45 with a gate row for each sequence), 4096 x 5120 layer norm of float32
+// rows 25 (5.0 TB/s), 8 x 4096 1.9 before and 2.8 after a block (latency: one trip to memory, 1 to 4
+// block-wide sums, one store).
 #include "block.cuh"
 #include "codes.cuh"
 #include "ptx.cuh"
@@ -345,8 +351,8 @@ cudaError_t launch_rows(const BlockNormArgs& a, int num_sms, cudaStream_t stream
   const int pieces = a.D / 8;
   if (pieces > max_threads<R>(kMaxPieces) * kMaxPieces)
     return launch(block_norm_long_kernel<T, R>, a.M, kLongThreads, stream, a);
-  // 1 / 2 / 4 pieces a thread, us: 2048 x 12288 after 65 / 65 / 48, 4096 x 4096 before 18.8 / 14.5 /
-  // 13.7, 128 x 4096 after 4.2 / 4.1 / 5.3, 1 x 4096 after 2.8 / 3.3 / 4.7
+  // 1 / 2 / 4 pieces a thread, us: 2048 x 12288 after 68 / 68 / 42, 4096 x 4096 before 19.1 / 16.0 /
+  // 13.2, 592 x 4096 after 7.0 / 5.5 / 5.3, 128 x 4096 3.7 / 4.3 / 4.2, 1 x 4096 3.1 / 3.7 / 3.9
   int nv = a.M >= num_sms * 4 ? 4 : 1;
   while ((pieces + nv - 1) / nv > max_threads<R>(nv)) nv *= 2;
   const int width = ((pieces + nv - 1) / nv + 31) / 32 * 32;
