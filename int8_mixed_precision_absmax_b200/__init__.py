@@ -491,19 +491,21 @@ def _at(t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: int, name: st
     raise ValueError(f"{name} must be contiguous")
 
 
-def _matrix(t: torch.Tensor, dtypes: tuple, name: str) -> int:
-    """The CUDA device of a contiguous matrix of one of the dtypes."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _matrix(t: torch.Tensor, dtypes: tuple, name: str) -> tuple:
+    """(CUDA device, rows, columns) of a contiguous matrix of one of the dtypes."""
+    if not isinstance(t, torch.Tensor) or (device := t.get_device()) < 0 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must have 2 dimensions")
-    if max(t.shape) > _INT_MAX:  # the library takes ints
-        raise ValueError(f"{name} has a size of 2^31 or more: {list(t.shape)}")
+    rows, columns = shape
+    if rows > _INT_MAX or columns > _INT_MAX:  # the library takes ints
+        raise ValueError(f"{name} has a size of 2^31 or more: {list(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.get_device()
+    return device, rows, columns
 
 
 def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
@@ -542,9 +544,8 @@ def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = 
     [N, K/2] (their order is in int8mm.h), one scale of W's type for every group_size input
     features, and, unless symmetric, one zero point (uint8) for each; zeros is None if
     symmetric."""
-    dev = _matrix(W, _HALF_TYPES, "W")
+    dev, N, K = _matrix(W, _HALF_TYPES, "W")
     T = W.dtype
-    N, K = W.shape
     shape = _int4_shapes(N, K, group_size)
     if symmetric and zeros is not None:
         raise ValueError("zeros is an output of the asymmetric quantizer: pass symmetric=False")
@@ -564,8 +565,7 @@ def int4_dequant_weight(codes: torch.Tensor, scales: torch.Tensor,
                         zeros: torch.Tensor | None = None, group_size: int = 128,
                         W_hat: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """What the codes stand for: scales * (code - zero) of scales' type, [N, K]."""
-    dev = _matrix(codes, (torch.uint8,), "codes")
-    N, K = codes.shape
+    dev, N, K = _matrix(codes, (torch.uint8,), "codes")
     K *= 2
     T = scales.dtype
     if T not in _HALF_TYPES:
@@ -586,9 +586,8 @@ def int4_linear_forward(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
                         dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X . W_hat^T + bias, [M, N] of X's type (fp16 or bf16), on the 4-bit weights of
     int4_quant_weight.  dev_status: an int32 that receives a device-side failure code."""
-    dev = _matrix(X, _HALF_TYPES, "X")
+    dev, M, K = _matrix(X, _HALF_TYPES, "X")
     T = X.dtype
-    M, K = X.shape
     N = codes.shape[0]
     shape = _int4_shapes(N, K, group_size)
     if Y is None:
@@ -609,9 +608,8 @@ def int8_block_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     """h = norm(x) * weight + bias for the rows of x [M, D]: the root-mean-square norm, or the
     layer norm (layer_norm=True).  x is fp16, bf16, or float32 (a residual stream kept in 32
     bits; h then has the type of weight, or of the h given, or fp16).  h may be x itself."""
-    dev = _matrix(x, _ROW_TYPES, "x")
+    dev, M, D = _matrix(x, _ROW_TYPES, "x")
     T = R = x.dtype
-    M, D = x.shape
     if R is torch.float32:
         T = weight.dtype if weight is not None else torch.float16 if h is None else h.dtype
         if T not in _HALF_TYPES:
@@ -642,10 +640,9 @@ def int8_block_residual(f: torch.Tensor, x: torch.Tensor, post_norm: bool = Fals
 
     f is fp16 or bf16; x has f's type or is float32, and y has x's.  gate is [Gr, D] or [D]: row
     m of f takes gate row m // (M / Gr).  y may be x itself, h may be f itself."""
-    dev = _matrix(f, _HALF_TYPES, "f")
+    dev, M, D = _matrix(f, _HALF_TYPES, "f")
     T, R = f.dtype, x.dtype
-    rows = M, D = f.shape
-    vector = (D,)
+    rows, vector = (M, D), (D,)
     if R is not T and R is not torch.float32:
         raise TypeError(f"x must be {T} like f, or float32, got {R}")
     if not post_norm and (post_weight is not None or post_bias is not None):
