@@ -116,8 +116,9 @@ struct Int4Values<__half> {
     z1 = 0xD400D400u + z * 0x00100010u;  // -64 - z, of a code in bits 4..7: (1024 + 16 u) / 16
   }
   static __device__ __forceinline__ __half2 of(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+  // u - z, exact; word: times the scale, rounded
   template <bool LOP3>
-  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+  __device__ __forceinline__ void offsets(uint32_t w, uint32_t* out) const {
     constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, k1024 = 0x64006400u;
     const uint32_t w8 = w >> 8;
     const uint32_t a[4] = {nibbles<LOP3>(w, kLow, k1024), nibbles<LOP3>(w, kHigh, k1024),
@@ -126,7 +127,15 @@ struct Int4Values<__half> {
     for (int i = 0; i < 4; ++i) {
       const __half2 d = (i & 1) ? __hfma2(of(a[i]), __float2half2_rn(0.0625f), of(z1))
                                 : __hsub2(of(a[i]), of(z0));
-      const __half2 v = __hmul2(d, of(s));
+      out[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+  }
+  template <bool LOP3>
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+    offsets<LOP3>(w, out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 v = __hmul2(of(out[i]), of(s));
       out[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
@@ -142,11 +151,20 @@ struct Int4Values<__nv_bfloat16> {
     return *reinterpret_cast<__nv_bfloat162*>(&v);
   }
   template <bool LOP3>
-  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+  __device__ __forceinline__ void offsets(uint32_t w, uint32_t* out) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t u = nibbles<LOP3>(w >> (4 * i), 0x000F000Fu, 0x43004300u);
-      const __nv_bfloat162 v = __hmul2(__hsub2(of(u), of(z0)), of(s));
+      const __nv_bfloat162 d =
+          __hsub2(of(nibbles<LOP3>(w >> (4 * i), 0x000F000Fu, 0x43004300u)), of(z0));
+      out[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+  }
+  template <bool LOP3>
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+    offsets<LOP3>(w, out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __hmul2(of(out[i]), of(s));
       out[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }

@@ -8,28 +8,26 @@
 // mma.sync almost as they lie in memory, the weights as the 16-row operand and the activations as
 // the 8 columns, in one of two ways.
 //
-// One or two tokens (kDigits): u8 x s8 MMAs.  One AND makes 4 operands of a word's low nibbles,
-// another 4 of its high nibbles (16 u; two accumulators keep the two apart and meet when a group
-// is scaled: 16 lo + hi).  The activations are written in three digits,
+// One token (DIGITS): u8 x s8 MMAs.  One AND makes 4 operands of a word's low nibbles, another 4 of
+// its high nibbles (16 u; two accumulators keep the two apart and meet when a group is scaled:
+// 16 lo + hi).  The activations are written in three digits,
 //   X = 2^e (65536 d2 + 256 d1 + d0),  d in -128..127,  2^(e+21) near the largest |X| of 256 columns
 // a fixed-point number of 23 bits, off by at most 2^-21 of that largest value (a float32 sum of its
-// products loses as much).  Three columns are one token, so all sums of a group are whole numbers
+// products loses as much).  Three columns are the token, so all sums of a group are whole numbers
 // and exact; scaled, they are summed in float32 column by column.  256 columns that hold a NaN or an
-// infinity have no such numbers: the token's results are NaN.
+// infinity have no such numbers: the results are NaN.  The zero point is taken out with the sum of
+// the group's digits, which one more MMA against ones gives in every row.
 //
-// Three to 8 tokens: 16-bit MMAs (the digits of more tokens would need more MMAs than the HBM rate
-// leaves time for: three tokens of 5120 x 13824 took 40 us with them, against 18).
-//   - fp16: a code in the low bits of a 16-bit half is a subnormal, u 2^-24 (bits 0-3) or u 2^-20
-//     (bits 4-7), which the tensor core multiplies exactly.  One AND gives two of them, so 8
-//     weights cost 4 ANDs and a shift, and no conversion.  Two accumulators keep the two powers
-//     apart and meet when a group is scaled: t = 16 lo + hi.
-//   - bf16 has no subnormals to spare (their products would be below float32's range): a code set
-//     into the mantissa of 128 reads as 128 + u, one AND-OR and a shift for two.
+// Two to 8 tokens: 16-bit MMAs on u - z, which is exact: a code set into the mantissa of 1024 (bf16:
+// 128) by one logic instruction, less that number and the zero point, for two weights at a time.  (MMAs
+// on the codes alone, the zero point by a sum of the activations, saved the subtractions but took
+// half as many MMAs again: 8 tokens of 4096 x 4096 6.9 us, against 6.2; 3 tokens of 13824 x 5120 18.3,
+// 17.1.  One token of 12288 x 49152 takes 74 us this way, 53 with digits; two tokens 74 with digits, 65
+// this way.)
 //
-// Either way the zero point (and the 128) is taken out with the sum of the group's activations,
-// which one more MMA against a constant gives in every row, and the group's scale meets the float32
-// sum of the group: the weights are never rounded.  Which k a lane takes is free as long as both
-// operands agree: lane t of a quad takes neighbouring words of its row.
+// Either way the group's scale meets the float32 sum of the group: the weights are never rounded.
+// Which k a lane takes is free as long as both operands agree: lane t of a quad takes neighbouring
+// words of its row.
 //
 // A block owns a range of 16-row units and takes them in pairs; its warps share the K axis in
 // chunks of 256 columns, each warp with a ring of its own that TMA fills (boxes of 16 or 32 rows x
@@ -39,11 +37,11 @@
 // every `batch` pairs, in an order that does not change.  (K split over the blocks of a cluster, to
 // even out few units, cost more in joining than it gave.)
 //
-// Measured, us: one token of 12288 x 49152, groups of 128, 52.6 (5.9 TB/s, 90 % of the measured copy
-// rate); one of 4096 x 4096 5.3 and 8 of 4096 x 4096, groups of 64 with zero points, 6.6 (1.4 TB/s: two
-// trips to memory, X and then the rest, and the launch); 3 of 13824 x 5120 18.3 (2.0 TB/s: 320 units
+// Measured, us: one token of 12288 x 49152, groups of 128, 51 (6.1 TB/s, 93 % of the measured copy
+// rate); one of 4096 x 4096 5.0 and 8 of 4096 x 4096, groups of 64 with zero points, 6.1 (1.5 TB/s: two
+// trips to memory, X and then the rest, and the launch); 3 of 13824 x 5120 17.1 (2.2 TB/s: 320 units
 // are 2 or 3 to a block, and with 4 warps a scheduler the latencies of a chunk's steps, loads to
-// operands to MMAs to scales, are not covered: issue slots are 31 % full, the tensor pipe 20 %).
+// operands to MMAs to scales, are not covered).
 #include <type_traits>
 
 #include "block.cuh"
@@ -268,12 +266,16 @@ template <typename T, int SUB, bool ZP, bool TWO>
 __device__ __forceinline__ void add_chunk_16(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t row,
                                           uint32_t swz, uint32_t x, int t, int src) {
   constexpr int U = TWO ? 2 : 1;
-  constexpr bool kHalf = std::is_same<T, __half>::value;
-  constexpr uint32_t kOne = kHalf ? 0x00100010u : 0x3F803F80u;  // 2^-20 or 1, twice
   const uint32_t x_t = x + 16u * SUB * t;
 #pragma unroll
   for (int j = 0; j < 8 / SUB; ++j) {
-    float lo[2][4], hi[2][4], sum[4];
+    // the block's zero points: rows g and g + 8 of each unit
+    Int4Values<T> q[4];
+#pragma unroll
+    for (int r = 0; r < 2 * U; ++r)
+      q[r].set(0, ZP ? __shfl_sync(~0u, rg.z[j / 4], src + 8 * r) >> (8 * (j & 3)) & 0xFFu
+                     : static_cast<uint32_t>(kInt4Zero));
+    float sum[2][2][4];  // of each unit, two for the MMAs to take in turn
     const uint32_t at = row + ((16u * SUB * j + 4u * SUB * t) ^ swz);
     uint32_t wa[2][SUB], wb[2][SUB];
 #pragma unroll
@@ -283,46 +285,24 @@ __device__ __forceinline__ void add_chunk_16(float (&acc)[2][4], const RowGroups
     }
 #pragma unroll
     for (int w = 0; w < SUB; ++w) {
-      const bool first = w == 0;
       uint32_t xr[4];
       lds<4>(xr, x_t + 64u * SUB * j + 16u * w);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const uint32_t a = wa[i][w], b = wb[i][w];
-        if constexpr (kHalf) {
-          // the activations' words lie in the order 0, 2, 1, 3
-          const uint32_t a8 = a >> 8, b8 = b >> 8;
-          mma_16x8x16<T>(lo[i], a & 0x000F000Fu, b & 0x000F000Fu, a8 & 0x000F000Fu,
-                         b8 & 0x000F000Fu, xr[0], xr[1], first);
-          mma_16x8x16<T>(hi[i], a & 0x00F000F0u, b & 0x00F000F0u, a8 & 0x00F000F0u,
-                         b8 & 0x00F000F0u, xr[2], xr[3], first);
-        } else {
-          constexpr uint32_t k128 = 0x43004300u;
-          mma_16x8x16<T>(lo[i], (a & 0x000F000Fu) | k128, (b & 0x000F000Fu) | k128,
-                         (a >> 4 & 0x000F000Fu) | k128, (b >> 4 & 0x000F000Fu) | k128, xr[0],
-                         xr[1], first);
-          mma_16x8x16<T>(lo[i], (a >> 8 & 0x000F000Fu) | k128, (b >> 8 & 0x000F000Fu) | k128,
-                         (a >> 12 & 0x000F000Fu) | k128, (b >> 12 & 0x000F000Fu) | k128, xr[2],
-                         xr[3], false);
-        }
+        uint32_t a[4], b[4];
+        q[2 * i].template offsets<true>(wa[i][w], a);
+        q[2 * i + 1].template offsets<true>(wb[i][w], b);
+        mma_16x8x16<T>(sum[i][0], a[0], b[0], a[1], b[1], xr[0], xr[1], w == 0);
+        mma_16x8x16<T>(sum[i][1], a[2], b[2], a[3], b[3], xr[2], xr[3], w == 0);
       }
-      mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[0], xr[1], first);
-      mma_16x8x16<T>(sum, kOne, kOne, kOne, kOne, xr[2], xr[3], false);
     }
-    // the block's scales: rows g and g + 8 of each unit
 #pragma unroll
     for (int r = 0; r < 2 * U; ++r) {
-      const uint32_t sw = __shfl_sync(~0u, rg.s[j / 2], src + 8 * r);
-      const float s = scale_value<T>(sw, j & 1);
-      float z = kInt4Zero;
-      if (ZP)
-        z = small_float(__shfl_sync(~0u, rg.z[j / 4], src + 8 * r) >> (8 * (j & 3)) & 0xFFu);
-      if (!kHalf) z += 128.0f;
+      const float s = scale_value<T>(__shfl_sync(~0u, rg.s[j / 2], src + 8 * r), j & 1);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = r / 2, d = 2 * (r & 1) + h;
-        const float v = kHalf ? fmaf(lo[i][d], 16.0f, hi[i][d]) : lo[i][d];
-        acc[i][d] = fmaf(s, fmaf(-z, sum[h], v), acc[i][d]);
+        acc[i][d] = fmaf(s, sum[i][0][d] + sum[i][1][d], acc[i][d]);
       }
     }
   }
@@ -358,12 +338,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(stream_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warps = blockDim.x / 32;
-  const int cols = DIGITS ? 3 * p.M : p.M;  // of the activations' operand: digit d of token m is 3 m + d
+  const int cols = DIGITS ? 3 : p.M;        // of the activations' operand: digits or tokens
   const int part_floats = 32 * cols;        // a warp's partial sums of a pair
   uint8_t* xs = ring + static_cast<size_t>(warps) * p.stages * kStageBytes;
   StreamShared& S = *reinterpret_cast<StreamShared*>(xs + static_cast<size_t>(cols) * p.xstride);
-  float* xscale = reinterpret_cast<float*>(&S + 1);  // DIGITS: 2^e, [token][chunk]
-  float* part = xscale + (DIGITS ? p.M * p.chunks : 0);
+  float* xscale = reinterpret_cast<float*>(&S + 1);  // DIGITS: 2^e of each chunk
+  float* part = xscale + (DIGITS ? p.chunks : 0);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   volatile int* abort = &S.abort;
@@ -418,15 +398,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 
   grid_dependency_wait();
   const int pieces = p.K / 8;  // 16 bytes, 8 columns; a lane takes one of each chunk and token
-  uint4 xv[2];                 // DIGITS: of the next chunk of the first pair
+  uint4 xv;                    // DIGITS: of the next chunk of the first pair
   auto load_x = [&](int chunk) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int i = chunk * 32 + lane;
-      xv[m] = (m < p.M && i < pieces)
-                  ? reinterpret_cast<const uint4*>(static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K)[i]
-                  : make_uint4(0, 0, 0, 0);
-    }
+    const int i = chunk * 32 + lane;
+    xv = i < pieces ? static_cast<const uint4*>(p.X)[i] : make_uint4(0, 0, 0, 0);
   };
   if constexpr (DIGITS) {
     if (q == 0) load_x(c);
@@ -458,55 +433,42 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (pair == 0) {
         // this chunk's activations, for every pair
         if constexpr (DIGITS) {
+          const uint4 v = xv;
+          // magnitudes of a 16-bit type compare as whole numbers
+          const uint32_t two = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                        __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+          const uint32_t most = __float_as_uint(
+              unpack2<T>(__reduce_max_sync(~0u, max(two & 0xFFFFu, two >> 16))).x);
+          const int e = -digit_exponent(most);
+          const float f1 = __int_as_float((127 + e / 2) << 23);
+          const float f2 = __int_as_float((127 + e - e / 2) << 23);
+          const float2 p01 = unpack2<T>(v.x), p23 = unpack2<T>(v.y), p45 = unpack2<T>(v.z),
+                       p67 = unpack2<T>(v.w);
+          // bytes of a word's low nibbles: columns 0, 4, 1, 5; of its high ones: 2, 6, 3, 7
+          const float low[4] = {p01.x, p45.x, p01.y, p45.y};
+          const float high[4] = {p23.x, p67.x, p23.y, p67.y};
+          uint32_t dl[3], dh[3];
+          digits4(low, f1, f2, dl);
+          digits4(high, f1, f2, dh);
+          // one word: its low nibbles' digits, then its high ones'; two words: both low, then both high
+          const int i = c * 32 + lane, at = SUB == 1 ? 2 * i : (i & ~1) * 2 + (i & 1);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (m < p.M) {
-              const uint4 v = xv[m];
-              // magnitudes of a 16-bit type compare as whole numbers
-              const uint32_t two = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                            __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-              const uint32_t most = __float_as_uint(
-                  unpack2<T>(__reduce_max_sync(~0u, max(two & 0xFFFFu, two >> 16))).x);
-              const int e = -digit_exponent(most);
-              const float f1 = __int_as_float((127 + e / 2) << 23);
-              const float f2 = __int_as_float((127 + e - e / 2) << 23);
-              const float2 p01 = unpack2<T>(v.x), p23 = unpack2<T>(v.y), p45 = unpack2<T>(v.z),
-                           p67 = unpack2<T>(v.w);
-              // bytes of a word's low nibbles: columns 0, 4, 1, 5; of its high ones: 2, 6, 3, 7
-              const float low[4] = {p01.x, p45.x, p01.y, p45.y};
-              const float high[4] = {p23.x, p67.x, p23.y, p67.y};
-              uint32_t dl[3], dh[3];
-              digits4(low, f1, f2, dl);
-              digits4(high, f1, f2, dh);
-              // one word: its low nibbles' digits, then its high ones'; two words: both low, then
-              // both high
-              const int i = c * 32 + lane, at = SUB == 1 ? 2 * i : (i & ~1) * 2 + (i & 1);
-#pragma unroll
-              for (int d = 0; d < 3; ++d) {
-                uint32_t* out =
-                    reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(3 * m + d) * p.xstride);
-                out[at] = dl[d];
-                out[at + (SUB == 1 ? 1 : 2)] = dh[d];
-              }
-              // 16 lo + hi is 16 times the sum
-              if (lane == 0)
-                xscale[m * p.chunks + c] = most >= 0x7F800000u ? __int_as_float(0x7FC00000)
-                                                               : ldexpf(SUB > 1 ? 0.0625f : 1.0f, -e);
-            }
+          for (int d = 0; d < 3; ++d) {
+            uint32_t* out = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(d) * p.xstride);
+            out[at] = dl[d];
+            out[at + (SUB == 1 ? 1 : 2)] = dh[d];
           }
+          // 16 lo + hi is 16 times the sum
+          if (lane == 0)
+            xscale[c] = most >= 0x7F800000u ? __int_as_float(0x7FC00000)
+                                            : ldexpf(SUB > 1 ? 0.0625f : 1.0f, -e);
           if (nq == 0) load_x(nc);
         } else {
           if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
           const int i = c * 32 + lane;
-          // The two operand words of an MMA are a register pair: of fp16 the words 0 and 2 of 16 bytes
-          // (the low nibbles' columns), then 1 and 3.  Zeros up to the chunk's end.
-          if (std::is_same<T, __half>::value || i >= pieces) {
-#pragma unroll 4
-            for (int m = 0; m < p.M; ++m) {
-              uint4* at = reinterpret_cast<uint4*>(xs + static_cast<size_t>(m) * p.xstride) + i;
-              const uint4 v = *at;
-              *at = i < pieces ? make_uint4(v.x, v.z, v.y, v.w) : make_uint4(0, 0, 0, 0);
-            }
+          if (i >= pieces) {  // zeros up to the chunk's end
+            for (int m = 0; m < p.M; ++m)
+              reinterpret_cast<uint4*>(xs + static_cast<size_t>(m) * p.xstride)[i] = make_uint4(0, 0, 0, 0);
           }
         }
         __syncwarp();
@@ -523,14 +485,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
           float chunk[2][4] = {};
           if (two) add_chunk_digits<T, SUB, ZP, true>(chunk, cur, w, 16u * gr, x, t, gr);
           else add_chunk_digits<T, SUB, ZP, false>(chunk, cur, w, 16u * gr, x, t, gr);
+          const float f = xscale[c];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = xscale[min((2 * t + h) / 3, p.M - 1) * p.chunks + c];
+          for (int r = 0; r < 2; ++r) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int d = 2 * (r & 1) + h;
-              acc[r / 2][d] = fmaf(f, chunk[r / 2][d], acc[r / 2][d]);
-            }
+            for (int d = 0; d < 4; ++d) acc[r][d] = fmaf(f, chunk[r][d], acc[r][d]);
           }
         } else {
           if (two) add_chunk_16<T, SUB, ZP, true>(acc, cur, w, 16u * gr, x, t, gr);
@@ -565,14 +524,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll 8
         for (int w = 0; w < warps; ++w) {
 #pragma unroll
-          for (int e = 0; e < 3; ++e) d[e] += sums[w * part_floats + (3 * m + e) * 32];
+          for (int e = 0; e < 3; ++e) d[e] += sums[w * part_floats + e * 32];
         }
         v = fmaf(d[2], 65536.0f, fmaf(d[1], 256.0f, d[0]));
       } else {
         v = 0.0f;
 #pragma unroll 8
         for (int w = 0; w < warps; ++w) v += sums[w * part_floats + m * 32];
-        if (std::is_same<T, __half>::value) v *= 1048576.0f;  // the sums are of 2^-20 u X
       }
       const int n = (u0 + 2 * from) * kUnitRows + lane;
       if (n < min(p.N, u1 * kUnitRows)) {
@@ -607,16 +565,17 @@ int sub_of(int group) { return group == 32 ? 1 : group == 64 ? 2 : 4; }
 // 16 warps brings the activations into shared memory once an SM and lets all warps share the chunks,
 // but with few of them a warp has one in a pair, and waits; two blocks of 8 also fill each other's
 // pauses.  (us of two blocks of 8 / one of 16 / one of 8; K = 4096: one token, N 4096 6.3 / 6.7 / 6.1,
-// N 32768 16.4 / 25.4 / 20.6, 6 tokens, N 4096 - / 7.4 / 6.9; K = 8192: one token, N 4096 9.3 / 8.4 / 8.7,
-// 3 tokens, N 32768 - / 36.7 / 42.0; K = 12288: one token, N 49152 56.3 / 53.5 / 70.0.)
+// N 32768 16.4 / 25.4 / 20.6, 3 tokens 5.9 / 6.6 / 6.0, 19.3 / 22.0 / 24.1, 6 tokens, N 4096 - / 7.0 /
+// 6.5; K = 8192: one token, N 4096 9.3 / 8.4 / 8.7, 3 tokens, N 32768 - / 35.4 / 40.0; K = 12288: one
+// token, N 49152 56.3 / 53.5 / 70.0, 3 tokens, N 32768 - / 48.3 / 55.5.)
 struct Shape { int warps, per_sm; };
 constexpr Shape kFewChunks[] = {{8, 2}, {8, 1}, {16, 1}}, kManyChunks[] = {{16, 1}, {8, 1}};
 constexpr int kMany = 32;
 
 bool plan_stream(int M, int K, int group, StreamPlan& s) {
   if (M > kMaxTok) return false;
-  const bool digits = M <= 2;
-  const int sub = sub_of(group), cols = digits ? 3 * M : M;
+  const bool digits = M == 1;
+  const int sub = sub_of(group), cols = digits ? 3 : M;
   const int chunks = (K + kChunkK - 1) / kChunkK;
   // a column's activations up to the last chunk's end, and a pad that sets the quads of two columns
   // apart: 8, 16 or 32 bytes a lane of digits, twice that in 16 bits
@@ -630,7 +589,7 @@ bool plan_stream(int M, int K, int group, StreamPlan& s) {
     const size_t most = shape.per_sm == 2 ? kSmemMost / 2 : kSmemMost;
     const size_t pair_bytes = static_cast<size_t>(s.warps) * 32 * cols * sizeof(float);
     const size_t fixed = 1024 + static_cast<size_t>(cols) * s.xstride + sizeof(StreamShared) +
-                         (digits ? M * chunks * sizeof(float) : 0);
+                         (digits ? chunks * sizeof(float) : 0);
     for (s.stages = kMaxStages; s.stages >= 2; --s.stages) {
       const size_t ring = static_cast<size_t>(s.warps) * s.stages * kStageBytes;
       for (s.batch = 4; s.batch >= 1; s.batch /= 2) {
@@ -675,7 +634,7 @@ cudaError_t launch_sub(const CUtensorMap (&map)[2], const StreamArgs& p, const S
 template <typename T>
 cudaError_t launch_typed(const CUtensorMap (&map)[2], const StreamArgs& p, const StreamPlan& s,
                          int grid, cudaStream_t stream) {
-  if (p.M <= 2)
+  if (p.M == 1)
     return p.zeros ? launch_sub<T, true, true>(map, p, s, grid, stream)
                    : launch_sub<T, false, true>(map, p, s, grid, stream);
   return p.zeros ? launch_sub<T, true, false>(map, p, s, grid, stream)
@@ -684,15 +643,15 @@ cudaError_t launch_typed(const CUtensorMap (&map)[2], const StreamArgs& p, const
 
 }  // namespace
 
-// With 4 tokens and more in one block of 8 warps, instructions bound the kernel, and many units to a
-// block are better off with the tensor cores.  (us of this / of int4_tile.cu, N = 4096, 11008, 32768;
-// K = 4096: 6 tokens 6.9 / 8.4, 13.0 / 12.8, 28.4 / 25.9, 8 tokens 7.1 / 8.5, 13.8 / 12.9, 30.6 / 26.1;
-// K = 12288: 4 tokens 13.8 / 13.3, 30.6 / 30.0, 68.3 / 66.8; two tokens 12.3 / 13.2, 26.5 / 29.7,
-// 50.4 / 66.8.)
+// Where the activations leave room for one block of 8 warps only, though they are of few columns (8
+// tokens), instructions bound the kernel, and many units to a block are better off with the tensor
+// cores.  (us of this / of int4_tile.cu, N = 11008, 32768; 8 tokens, K = 2048 8.6 / 9.6, 17.6 / 15.2,
+// K = 4096 12.7 / 12.8, 27.7 / 26.0, K = 8192 21.1 / 21.6, 44.9 / 46.5; 6 tokens, K = 4096 12.0 / 12.8,
+// 25.7 / 25.9; 4 tokens, K = 12288 27.2 / 29.8, 59.5 / 66.8.)
 bool int4_stream_suits(int M, int N, int K, int group, int num_sms) {
   StreamPlan s;
   if (!plan_stream(M, K, group, s)) return false;
-  return M < 4 || s.warps * s.per_sm > 8 || N <= 4 * kUnitRows * num_sms;
+  return s.warps * s.per_sm > 8 || K / kChunkK >= kMany || N <= 8 * kUnitRows * num_sms;
 }
 
 cudaError_t launch_int4_stream(const Int4LinearArgs& a, int num_sms, cudaStream_t stream) {
