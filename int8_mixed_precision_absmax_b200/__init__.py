@@ -508,12 +508,20 @@ def _matrix(t: torch.Tensor, dtypes: tuple, name: str) -> tuple:
     return device, rows, columns
 
 
-def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """An output tensor on like's device whose memory belongs to the stream that the call runs on."""
+def _out(t: torch.Tensor | None, like: torch.Tensor, dtype, shape: tuple, device: int, name: str,
+         stream) -> tuple:
+    """(the output matrix, its address): t, or a new one on like's device whose memory belongs to
+    the stream that the call runs on.  (With its strides given torch makes it in 1.6 us, with
+    new_empty in 2.2.)"""
+    if t is not None:
+        return t, _at(t, dtype, shape, device, name)
+    strides = (shape[1], 1)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        t = torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
 
 
 def _call(what: str, device: int, stream, *args) -> None:
@@ -549,15 +557,13 @@ def int4_quant_weight(W: torch.Tensor, group_size: int = 128, symmetric: bool = 
     shape = _int4_shapes(N, K, group_size)
     if symmetric and zeros is not None:
         raise ValueError("zeros is an output of the asymmetric quantizer: pass symmetric=False")
-    if codes is None:
-        codes = _new(W, (N, K // 2), torch.uint8, stream)
-    if scales is None:
-        scales = _new(W, shape, T, stream)
-    if zeros is None and not symmetric:
-        zeros = _new(W, shape, torch.uint8, stream)
+    codes, codes_at = _out(codes, W, torch.uint8, (N, K // 2), dev, "codes", stream)
+    scales, scales_at = _out(scales, W, T, shape, dev, "scales", stream)
+    zeros_at = None
+    if not symmetric:
+        zeros, zeros_at = _out(zeros, W, torch.uint8, shape, dev, "zeros", stream)
     _call("int4_quant_weight", dev, stream, W.data_ptr(), N, K, group_size, T is torch.bfloat16,
-          _at(codes, torch.uint8, (N, K // 2), dev, "codes"), _at(scales, T, shape, dev, "scales"),
-          None if symmetric else _at(zeros, torch.uint8, shape, dev, "zeros"))
+          codes_at, scales_at, zeros_at)
     return codes, scales, zeros
 
 
@@ -571,12 +577,11 @@ def int4_dequant_weight(codes: torch.Tensor, scales: torch.Tensor,
     if T not in _HALF_TYPES:
         raise TypeError(f"scales must be torch.float16 or torch.bfloat16, got {T}")
     shape = _int4_shapes(N, K, group_size)
-    if W_hat is None:
-        W_hat = _new(codes, (N, K), T, stream)
+    W_hat, W_hat_at = _out(W_hat, codes, T, (N, K), dev, "W_hat", stream)
     _call("int4_dequant_weight", dev, stream, codes.data_ptr(),
           _at(scales, T, shape, dev, "scales"),
           None if zeros is None else _at(zeros, torch.uint8, shape, dev, "zeros"), N, K,
-          group_size, T is torch.bfloat16, _at(W_hat, T, (N, K), dev, "W_hat"))
+          group_size, T is torch.bfloat16, W_hat_at)
     return W_hat
 
 
@@ -590,13 +595,12 @@ def int4_linear_forward(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     T = X.dtype
     N = codes.shape[0]
     shape = _int4_shapes(N, K, group_size)
-    if Y is None:
-        Y = _new(X, (M, N), T, stream)
+    Y, Y_at = _out(Y, X, T, (M, N), dev, "Y", stream)
     _call("int4_linear_forward", dev, stream, X.data_ptr(), M, K,
           _at(codes, torch.uint8, (N, K // 2), dev, "codes"), _at(scales, T, shape, dev, "scales"),
           None if zeros is None else _at(zeros, torch.uint8, shape, dev, "zeros"),
           None if bias is None else _at(bias, T, (N,), dev, "bias"), N, group_size,
-          T is torch.bfloat16, _at(Y, T, (M, N), dev, "Y"),
+          T is torch.bfloat16, Y_at,
           None if dev_status is None else _at(dev_status, torch.int32, (1,), dev, "dev_status"))
     return Y
 
@@ -614,14 +618,12 @@ def int8_block_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
         T = weight.dtype if weight is not None else torch.float16 if h is None else h.dtype
         if T not in _HALF_TYPES:
             raise TypeError(f"weight and h must be torch.float16 or torch.bfloat16, got {T}")
-    if h is None:
-        h = _new(x, (M, D), T, stream)
+    h, h_at = _out(h, x, T, (M, D), dev, "h", stream)
     flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
              | (0 if R is T else _F32_RESIDUAL))
     _call("int8_block_norm", dev, stream, x.data_ptr(), M, D,
           None if weight is None else _at(weight, T, (D,), dev, "weight"),
-          None if bias is None else _at(bias, T, (D,), dev, "bias"), eps, flags,
-          _at(h, T, (M, D), dev, "h"))
+          None if bias is None else _at(bias, T, (D,), dev, "bias"), eps, flags, h_at)
     return h
 
 
@@ -659,10 +661,10 @@ def int8_block_residual(f: torch.Tensor, x: torch.Tensor, post_norm: bool = Fals
             gate_at = _at(gate, T, (gate_rows, D), dev, "gate")
         else:
             gate_rows, gate_at = 1, _at(gate, T, vector, dev, "gate")
-    if y is None:
-        y = _new(f, rows, R, stream)
-    if h is None and next_norm:
-        h = _new(f, rows, T, stream)
+    y, y_at = _out(y, f, R, rows, dev, "y", stream)
+    h_at = None
+    if next_norm:
+        h, h_at = _out(h, f, T, rows, dev, "h", stream)
     flags = ((_BFLOAT16 if T is torch.bfloat16 else 0) | (_LAYER_NORM if layer_norm else 0)
              | (0 if R is T else _F32_RESIDUAL) | (_POST_NORM if post_norm else 0))
     _call("int8_block_residual", dev, stream, f.data_ptr(), _at(x, R, rows, dev, "x"), M, D,
@@ -671,7 +673,7 @@ def int8_block_residual(f: torch.Tensor, x: torch.Tensor, post_norm: bool = Fals
           gate_at, gate_rows, x_scale, f_scale,
           None if next_weight is None else _at(next_weight, T, vector, dev, "next_weight"),
           None if next_bias is None else _at(next_bias, T, vector, dev, "next_bias"), eps, flags,
-          _at(y, R, rows, dev, "y"), None if h is None else _at(h, T, rows, dev, "h"))
+          y_at, h_at)
     return y, h
 
 
