@@ -13,8 +13,8 @@
 // against 48 then): it leaves fewer threads, and instructions were what bound it; packed float32
 // halves the arithmetic.
 //
-// Measured, us: 2048 x 12288 after a block, norm of f, gate of every channel, 41 (4.9 TB/s, 74 % of
-// the measured copy rate; 45 with a gate row for each sequence), 4096 x 5120 layer norm of float32
+// Measured, us: 2048 x 12288 after a block, norm of f, gate of every channel, 39 (5.2 TB/s, 79 % of
+// the measured copy rate; 43 with a gate row for each sequence), 4096 x 5120 layer norm of float32
 // rows 25 (5.0 TB/s), 8 x 4096 1.9 before and 2.8 after a block (latency: one trip to memory, 1 to 4
 // block-wide sums, one store).
 #include "block.cuh"
@@ -32,6 +32,20 @@ __host__ __device__ constexpr int max_threads(int nv) {
   return nv * static_cast<int>(sizeof(R)) > 8 ? 512 : 1024;
 }
 constexpr int kLongThreads = 1024;
+// Blocks of 384 threads and a little less: with 56 registers a thread (80 with float32 rows), 3 of them
+// fit on an SM (2), not 2 (1).  2048 x 12288 after a block, 16-bit rows 45.0 -> 42.7 us, float32 rows
+// 71.7 -> 67.7; other widths gain no block, or lose by it (4096 x 4096 26.9 -> 27.4).
+constexpr int kTight = 8;  // of KIND
+constexpr int kTightThreads = 384;
+inline bool tight_width(int width) { return width > 341 && width <= kTightThreads; }
+template <typename R>
+__host__ __device__ constexpr int threads_bound(int nv, int kind) {
+  return kind & kTight ? kTightThreads : max_threads<R>(nv);
+}
+template <typename R>
+__host__ __device__ constexpr int blocks_bound(int kind) {
+  return kind & kTight ? (sizeof(R) == 4 ? 2 : 3) : 0;  // 0: no bound
+}
 
 // 8 neighbours.
 template <typename V>
@@ -160,9 +174,10 @@ __device__ __forceinline__ float row_sum(float v, float* red, int first_warp, in
 // One row for every `width` threads (whole warps), NV pieces of 8 elements a thread.
 // KIND: 0 any call; otherwise the usual one, whose norms have weights (and biases just if they are
 // layer norms), whose x_scale is 1 and whose results are all wanted: 1, and 2 more with a norm of f,
-// and 4 more with a gate.
+// and 4 more with a gate; kTight more in blocks of that width.
 template <typename T, typename R, int NV, bool AFTER, bool LAYER, int KIND>
-__global__ void __launch_bounds__(max_threads<R>(NV)) block_norm_kernel(const BlockNormArgs a, int width) {
+__global__ void __launch_bounds__(threads_bound<R>(NV, KIND), blocks_bound<R>(KIND))
+    block_norm_kernel(const BlockNormArgs a, int width) {
   constexpr bool STD = KIND != 0;
   __shared__ float red[4][32];
   grid_launch_dependents();
@@ -367,11 +382,16 @@ cudaError_t launch_rows(const BlockNormArgs& a, int num_sms, cudaStream_t stream
     if constexpr (!AFTER) {
       return run(block_norm_kernel<T, R, 4, AFTER, LAYER, 1>);
     } else if (a.y && (!a.post_norm || usual(a.post_w, a.post_b))) {
+      auto kind = [&](auto plain, auto tight) { return run(tight_width(width) ? tight : plain); };
       if (a.post_norm)
-        return a.gate ? run(block_norm_kernel<T, R, 4, AFTER, LAYER, 7>)
-                      : run(block_norm_kernel<T, R, 4, AFTER, LAYER, 3>);
-      return a.gate ? run(block_norm_kernel<T, R, 4, AFTER, LAYER, 5>)
-                    : run(block_norm_kernel<T, R, 4, AFTER, LAYER, 1>);
+        return a.gate ? kind(block_norm_kernel<T, R, 4, AFTER, LAYER, 7>,
+                             block_norm_kernel<T, R, 4, AFTER, LAYER, 7 + kTight>)
+                      : kind(block_norm_kernel<T, R, 4, AFTER, LAYER, 3>,
+                             block_norm_kernel<T, R, 4, AFTER, LAYER, 3 + kTight>);
+      return a.gate ? kind(block_norm_kernel<T, R, 4, AFTER, LAYER, 5>,
+                           block_norm_kernel<T, R, 4, AFTER, LAYER, 5 + kTight>)
+                    : kind(block_norm_kernel<T, R, 4, AFTER, LAYER, 1>,
+                           block_norm_kernel<T, R, 4, AFTER, LAYER, 1 + kTight>);
     }
   }
   return run(block_norm_kernel<T, R, 4, AFTER, LAYER, 0>);

@@ -351,3 +351,10 @@ def test_sizes_past_an_int_are_refused():
         i8.int8_block_norm(torch.empty(2 ** 32 + 1, 0, dtype=torch.float16, device="cuda"))
     with pytest.raises(ValueError, match="2\\^31"):
         i8.int8_block_norm(torch.empty(0, 2 ** 32 + 16, dtype=torch.float16, device="cuda"))
+
+
+@pytest.mark.parametrize("T,R", TYPES)
+@pytest.mark.parametrize("D", [11008, 12288])
+def test_usual_calls_of_rows_of_384_threads(T, R, D):
+    """Rows whose blocks keep to fewer registers, three to an SM."""
+    test_usual_calls_of_many_rows(T, R, 604, D)
