@@ -359,7 +359,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   for (int i = threadIdx.x; i < p.chunks; i += blockDim.x) mbar_init(&S.x_ready[i], 1);
   fence_mbarrier_init();
   __syncthreads();
-  grid_launch_dependents();
 
   const int u0 = static_cast<int>(static_cast<long long>(p.units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<long long>(p.units) * (blockIdx.x + 1) / gridDim.x);
@@ -397,6 +396,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   if (q < pairs) load_groups<SUB, ZP>(nxt, p, (u0 + 2 * q) * kUnitRows + lane, c * kChunkK);
 
   grid_dependency_wait();
+  grid_launch_dependents();  // not before the wait: the launch after this one would reach back past it
   const int pieces = p.K / 8;  // 16 bytes, 8 columns; a lane takes one of each chunk and token
   uint4 xv;                    // DIGITS: of the next chunk of the first pair
   auto load_x = [&](int chunk) {

@@ -180,7 +180,6 @@ __global__ void __launch_bounds__(threads_bound<R>(NV, KIND), blocks_bound<R>(KI
     block_norm_kernel(const BlockNormArgs a, int width) {
   constexpr bool STD = KIND != 0;
   __shared__ float red[4][32];
-  grid_launch_dependents();
   const bool post = STD ? (KIND & 2) != 0 : a.post_norm, gated = STD ? (KIND & 4) != 0 : a.gate != nullptr;
   const int warps = width / 32, in_block = threadIdx.x / width, tid = threadIdx.x % width;
   const int first_warp = in_block * warps;
@@ -193,6 +192,7 @@ __global__ void __launch_bounds__(threads_bound<R>(NV, KIND), blocks_bound<R>(KI
 #pragma unroll
   for (int i = 0; i < NV; ++i) ok[i] = row_ok && tid + i * width < pieces;
   grid_dependency_wait();
+  grid_launch_dependents();  // not before the wait: the launch after this one would reach back past it
 
   // The row stays packed between its passes: f and x, then y in x's place.
   Piece<R> xp[NV];
@@ -289,7 +289,6 @@ template <typename T, typename R>
 __global__ void __launch_bounds__(kLongThreads) block_norm_long_kernel(const BlockNormArgs a) {
   __shared__ float red[4][kLongThreads / 32];
   constexpr int kWarps = kLongThreads / 32;
-  grid_launch_dependents();
   const long long m = blockIdx.x, at = m * a.D;
   const int pieces = a.D / 8;
   const float inv_d = 1.0f / static_cast<float>(a.D);
@@ -297,6 +296,7 @@ __global__ void __launch_bounds__(kLongThreads) block_norm_long_kernel(const Blo
   const R* x = static_cast<const R*>(a.x) + at;
   const T* gate = a.gate ? static_cast<const T*>(a.gate) + m / a.rows_per_gate * a.D : nullptr;
   grid_dependency_wait();
+  grid_launch_dependents();
 
   // mean and reciprocal deviation of the row whose piece c is piece(c)
   auto statistics = [&](auto piece, float* red0, float* red1, float& mean, float& r) {
