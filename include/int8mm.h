@@ -374,9 +374,8 @@ int int4_dequant_weight(const uint8_t *codes, const void *scales, const uint8_t 
  * With one or two tokens the products are of the codes themselves, where the activations fit into one
  * SM's shared memory; up to M = 8, as the sizes decide, of these or of W_hat rounded to T; beyond, of
  * W_hat rounded to T, which has to be finite.
- * As with int8_linear_forward, the weights may be read before the launch before this one on the
- * stream is done: codes, scales and zeros must not be written by a kernel launched just before
- * that lets its successors start early (int4_quant_weight and ordinary kernels do not).
+ * Nothing is read before the launches before this one on the stream are done: unlike Wq of
+ * int8_linear_forward, codes, scales and zeros may be written by the launch just before.
  */
 int int4_linear_forward(const void *X, int M, int K, const uint8_t *codes, const void *scales,
                         const uint8_t *zeros, const void *bias, int N, int group, unsigned flags,

@@ -31,8 +31,8 @@
 //
 // A block owns a range of 16-row units and takes them in pairs; its warps share the K axis in
 // chunks of 256 columns, each warp with a ring of its own that TMA fills (boxes of 16 or 32 rows x
-// 128 bytes, 128-byte swizzle).  The first chunks are requested before the wait for the previous
-// launch.  The warp that takes a chunk of the first pair brings that chunk's activations into shared
+// 128 bytes, 128-byte swizzle).  Before the wait for the previous launch, which may have made the
+// weights, the first chunks are brought as far as L2.  The warp that takes a chunk of the first pair brings that chunk's activations into shared
 // memory for all pairs, so nothing waits for the whole of X.  Partial sums meet in shared memory
 // every `batch` pairs, in an order that does not change.  (K split over the blocks of a cluster, to
 // even out few units, cost more in joining than it gave.)
@@ -391,9 +391,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   };
   settle(fp, fc);
   int q = fp, c = fc;  // the next chunk to multiply
-  for (int s = 0; s < p.stages; ++s) request();
+  // The weights may be the launch before's, so only L2, which sees its writes, gets them early.
+  for (int s = 0, eq = q, ec = c; s < p.stages && eq < pairs; ++s) {
+    const int u = u0 + 2 * eq;
+    if (lane == 0)
+      tma_prefetch_2d(u + 1 < u1 ? &map_pair : &map_unit, ec * (kChunkK / 2), u * kUnitRows);
+    ec += warps;
+    settle(eq, ec);
+  }
   RowGroups<SUB> cur, nxt;
-  if (q < pairs) load_groups<SUB, ZP>(nxt, p, (u0 + 2 * q) * kUnitRows + lane, c * kChunkK);
+  if (q < pairs) {
+    const long long at = static_cast<long long>(min((u0 + 2 * q) * kUnitRows + lane, p.N - 1)) * p.groups +
+                         c * kChunkK / p.group;
+    prefetch_l2(static_cast<const uint16_t*>(p.scales) + at);
+    if (ZP) prefetch_l2(p.zeros + at);
+  }
 
   grid_dependency_wait();
   grid_launch_dependents();  // not before the wait: the launch after this one would reach back past it
@@ -412,6 +424,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       bulk_load(xs + static_cast<size_t>(m) * p.xstride,
                 static_cast<const T*>(p.X) + static_cast<size_t>(m) * p.K, bytes, &S.x_full);
   }
+  for (int s = 0; s < p.stages; ++s) request();
+  if (q < pairs) load_groups<SUB, ZP>(nxt, p, (u0 + 2 * q) * kUnitRows + lane, c * kChunkK);
 
   // Row g of an MMA is row `gr` of the unit, the bits of g reversed: the rows that read shared
   // memory together then differ in the swizzle's high bits (conflict-free for 4, 8 and 16 bytes).

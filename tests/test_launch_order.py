@@ -53,3 +53,19 @@ def test_a_kernel_waits_before_its_successor_may_start(name):
         if LET_START in body:
             assert body.count(WAIT) == 1, kernel
             assert body.index(WAIT) < body.index(LET_START), kernel
+
+
+def test_the_streaming_product_reads_nothing_before_the_wait():
+    """Its weights may be what the launch before writes: before the wait they are only brought to L2."""
+    body = kernels("int4_stream.cu")["int4_stream_kernel"]
+    # what runs there: lambdas are defined, not called
+    early = body[:body.index(WAIT)]
+    lambdas = re.compile(r"auto \w+ = \[&\]\([^)]*\) \{.*?\n  \};", re.S)
+    assert len(lambdas.findall(early)) == 2
+    early = lambdas.sub("", early)
+    early = "".join(line for line in early.splitlines(True) if "prefetch_l2(" not in line)
+    for read in ("request(", "load_groups", "tma_load", "bulk_load", "load_x", "p.X", "p.bias",
+                 "p.scales", "p.zeros"):
+        assert read not in early, read
+    late = body[body.index(WAIT):]
+    assert "request();" in late and "load_groups<SUB, ZP>(nxt" in late
