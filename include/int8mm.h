@@ -371,9 +371,9 @@ int int4_dequant_weight(const uint8_t *codes, const void *scales, const uint8_t 
  * No workspace: calls on different streams do not disturb each other.
  * A NaN or an infinity in a row of X makes the results of that row NaN or infinite (which of the
  * two is not said); so may bfloat16 values of 2^112 and above, whose float32 sums can overflow.
- * With one or two tokens the products are of the codes themselves, where the activations fit into one
- * SM's shared memory; up to M = 8, as the sizes decide, of these or of W_hat rounded to T; beyond, of
- * W_hat rounded to T, which has to be finite.
+ * Up to M = 8, where the activations fit into one SM's shared memory and as the sizes decide, the
+ * products are of X and u - zero, both as they are, and the scale meets the float32 sum of its group;
+ * beyond, of X and W_hat rounded to T, which has to be finite.
  * Nothing is read before the launches before this one on the stream are done: unlike Wq of
  * int8_linear_forward, codes, scales and zeros may be written by the launch just before.
  */

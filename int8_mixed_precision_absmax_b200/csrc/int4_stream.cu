@@ -10,13 +10,18 @@
 //
 // One token (DIGITS): u8 x s8 MMAs.  One AND makes 4 operands of a word's low nibbles, another 4 of
 // its high nibbles (16 u; two accumulators keep the two apart and meet when a group is scaled:
-// 16 lo + hi).  The activations are written in three digits,
-//   X = 2^e (65536 d2 + 256 d1 + d0),  d in -128..127,  2^(e+21) near the largest |X| of 256 columns
-// a fixed-point number of 23 bits, off by at most 2^-21 of that largest value (a float32 sum of its
-// products loses as much).  Three columns are the token, so all sums of a group are whole numbers
-// and exact; scaled, they are summed in float32 column by column.  256 columns that hold a NaN or an
-// infinity have no such numbers: the results are NaN.  The zero point is taken out with the sum of
-// the group's digits, which one more MMA against ones gives in every row.
+// 16 lo + hi).  The activations of a chunk of 256 columns are written in five digits,
+//   X = 2^e (256^4 d4 + 256^3 d3 + 256^2 d2 + 256 d1 + d0),  d in -128..127,
+// 2^(e+38) near the chunk's largest |X|: whole numbers of 40 bits.  Five of the MMA's eight columns are
+// the token, so all sums of a group are whole numbers and exact; scaled, they are summed in float32
+// column by column, and at a pair's end over the columns.  The zero point is taken out with the sum of
+// the group's digits, which one more MMA against ones gives in every row; where u = z a column adds
+// exactly 0, however large.  Only exact digits are used: a chunk that has none (fp16: its largest
+// value is 32640 or more and another has bits below 2^e; bf16: one is below about 2^-31 of the
+// largest; a NaN or an infinity) keeps its activations in 16 bits and is multiplied like a chunk of
+// two tokens.  (Three digits, rounded, took 5.3 us for 4096 x 4096 and 51 for 12288 x 49152, against 5.9
+// and 53, but were wrong: where the largest column has the weight 0, all others had lost what is below
+// 2^-22 of it.)
 //
 // Two to 8 tokens: 16-bit MMAs on u - z, which is exact: a code set into the mantissa of 1024 (bf16:
 // 128) by one logic instruction, less that number and the zero point, for two weights at a time.  (MMAs
@@ -37,14 +42,15 @@
 // every `batch` pairs, in an order that does not change.  (K split over the blocks of a cluster, to
 // even out few units, cost more in joining than it gave.)
 //
-// Measured, us: one token of 12288 x 49152, groups of 128, 51 (6.1 TB/s, 93 % of the measured copy
-// rate); one of 4096 x 4096 5.0 and 8 of 4096 x 4096, groups of 64 with zero points, 6.1 (1.5 TB/s: two
-// trips to memory, X and then the rest, and the launch); 3 of 13824 x 5120 17.1 (2.2 TB/s: 320 units
+// Measured, us: one token of 12288 x 49152, groups of 128, 53 (5.9 TB/s, 90 % of the measured copy
+// rate); one of 4096 x 4096 5.9 and 8 of 4096 x 4096, groups of 64 with zero points, 6.4 (1.5 TB/s: two
+// trips to memory, X and then the rest, and the launch); 3 of 13824 x 5120 18.6 (2.0 TB/s: 320 units
 // are 2 or 3 to a block, and with 4 warps a scheduler the latencies of a chunk's steps, loads to
 // operands to MMAs to scales, are not covered).
 #include <type_traits>
 
 #include "block.cuh"
+#include "codes.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -53,6 +59,7 @@ namespace i8mm {
 namespace {
 
 constexpr int kMaxTok = 8;
+constexpr int kDigits = 5;
 constexpr int kUnitRows = 16;
 constexpr int kChunkK = 256;                        // columns of a chunk: 128 bytes of a row
 constexpr int kUnitBytes = kUnitRows * kChunkK / 2;
@@ -261,10 +268,11 @@ __device__ __forceinline__ void add_chunk_digits(float (&acc)[2][4], const RowGr
   }
 }
 
-// The same with 16-bit operands; x: the lane's token's activations at the chunk's start.
+// The same with 16-bit operands; x: the lane's token's activations at the chunk's start, those from
+// byte 256 on `gap` bytes further.
 template <typename T, int SUB, bool ZP, bool TWO>
 __device__ __forceinline__ void add_chunk_16(float (&acc)[2][4], const RowGroups<SUB>& rg, uint32_t row,
-                                          uint32_t swz, uint32_t x, int t, int src) {
+                                          uint32_t swz, uint32_t x, uint32_t gap, int t, int src) {
   constexpr int U = TWO ? 2 : 1;
   const uint32_t x_t = x + 16u * SUB * t;
 #pragma unroll
@@ -286,7 +294,7 @@ __device__ __forceinline__ void add_chunk_16(float (&acc)[2][4], const RowGroups
 #pragma unroll
     for (int w = 0; w < SUB; ++w) {
       uint32_t xr[4];
-      lds<4>(xr, x_t + 64u * SUB * j + 16u * w);
+      lds<4>(xr, x_t + 64u * SUB * j + (64 * SUB * j >= 256 ? gap : 0u) + 16u * w);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         uint32_t a[4], b[4];
@@ -308,24 +316,56 @@ __device__ __forceinline__ void add_chunk_16(float (&acc)[2][4], const RowGroups
   }
 }
 
-// e of the digits, from the float bits of the largest magnitude: that becomes 2^21 .. 1.97 * 2^21 (or
-// a little less), so that 0x8080 may be added below 2^22.  -148 .. 107.
-__device__ __forceinline__ int digit_exponent(uint32_t most) {
-  return static_cast<int>((most + 0x40000u) >> 23) - 127 - 21;
+__device__ __forceinline__ float power_of_2(int e) {  // of a normal number
+  return __int_as_float((127 + e) << 23);
 }
 
-// The digits of 4 activations, scaled by f1 f2 to below 2^22 in magnitude: one word for each digit.
-// Rounded into the mantissa of kMagic, to nearest; with 0x8080 added, the number's low bytes are
-// d0 + 128 and d1 + 128, and the third is d2 + 64.
-__device__ __forceinline__ void digits4(const float (&f)[4], float f1, float f2, uint32_t (&d)[3]) {
-  uint32_t v[4];
+// The digits' unit 2^e of a chunk from its largest magnitude `most` and its smallest but 0, 0x8000 -
+// `least` (their bits in T): most becomes 1 .. 1.992 * 2^38, since digits of -128..127 reach
+// 0x7F7F7F7F7F = 1.992 * 2^38.  exact: no value has bits below the unit.
+template <typename T>
+__device__ __forceinline__ int digit_exponent(uint32_t most, uint32_t least, bool& exact) {
+  const uint32_t f = __float_as_uint(unpack2<T>(most).x);
+  const int e = max(static_cast<int>((f + 0x10000u) >> 23) - 127 - 38, -126);
+  if (std::is_same<T, __half>::value)  // 2^-24 is the type's own unit
+    exact = e <= -24;
+  else  // the last of the smallest one's 7 bits; 0 alone: least = 0, which is 2^128
+    exact = e <= max(static_cast<int>((0x8000u - least) >> 7), 1) - 127 - 7;
+  return e;
+}
+
+// The digits of 4 activations with the unit 2^e, one word for each digit: with 128 added to each digit,
+// they are the bytes of a whole number h 2^20 + l.  Rounded into the mantissa of kMagic, h and l are
+// whole numbers below 2^20.
+__device__ __forceinline__ void digits4(const uint64_t (&f)[2], int e, uint32_t (&d)[kDigits]) {
+  constexpr long long kBias = 0x8080808080ll - (static_cast<long long>(kMagicBits) << 20) - kMagicBits;
+  const float h1 = power_of_2(-e - 20), h0 = -power_of_2(e + 20), l1 = power_of_2(-e);
+  const uint64_t magic = f32x2_pack(kMagic, kMagic), minus = f32x2_pack(-kMagic, -kMagic);
+  uint32_t lo[4], hi[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(fmaf(f[i] * f1, f2, kMagic + 32896.0f));
-  const uint32_t a = __byte_perm(v[0], v[1], 0x5140), b = __byte_perm(v[2], v[3], 0x5140);
-  d[0] = __byte_perm(a, b, 0x5410) ^ 0x80808080u;
-  d[1] = __byte_perm(a, b, 0x7632) ^ 0x80808080u;
-  const uint32_t c = __byte_perm(__byte_perm(v[0], v[1], 0x0062), __byte_perm(v[2], v[3], 0x0062), 0x5410);
-  d[2] = ((c | 0x80808080u) - 0x40404040u) ^ 0x80808080u;  // c - 64, byte by byte
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t h = f32x2_fma(f[i], f32x2_pack(h1, h1), magic);
+    const uint64_t rest = f32x2_fma(f32x2_add(h, minus), f32x2_pack(h0, h0), f[i]);
+    const uint64_t l = f32x2_fma(rest, f32x2_pack(l1, l1), magic);
+    uint32_t hb[2], lb[2];
+    f32x2_unpack(h, hb[0], hb[1]);
+    f32x2_unpack(l, lb[0], lb[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const unsigned long long b =
+          static_cast<unsigned long long>(kBias + static_cast<long long>(static_cast<int>(hb[k])) * (1 << 20)) + lb[k];
+      lo[2 * i + k] = static_cast<uint32_t>(b);
+      hi[2 * i + k] = static_cast<uint32_t>(b >> 32);
+    }
+  }
+  const uint32_t a0 = __byte_perm(lo[0], lo[1], 0x5140), a1 = __byte_perm(lo[2], lo[3], 0x5140);
+  const uint32_t b0 = __byte_perm(lo[0], lo[1], 0x7362), b1 = __byte_perm(lo[2], lo[3], 0x7362);
+  d[0] = __byte_perm(a0, a1, 0x5410) ^ 0x80808080u;
+  d[1] = __byte_perm(a0, a1, 0x7632) ^ 0x80808080u;
+  d[2] = __byte_perm(b0, b1, 0x5410) ^ 0x80808080u;
+  d[3] = __byte_perm(b0, b1, 0x7632) ^ 0x80808080u;
+  d[4] = __byte_perm(__byte_perm(hi[0], hi[1], 0x0040), __byte_perm(hi[2], hi[3], 0x0040), 0x5410) ^
+         0x80808080u;
 }
 
 }  // namespace
@@ -338,11 +378,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(stream_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warps = blockDim.x / 32;
-  const int cols = DIGITS ? 3 : p.M;        // of the activations' operand: digits or tokens
-  const int part_floats = 32 * cols;        // a warp's partial sums of a pair
+  const int cols = DIGITS ? kDigits : p.M;  // of the activations' operand: digits or tokens
+  const int part_floats = 32 * p.M;         // a warp's partial sums of a pair
   uint8_t* xs = ring + static_cast<size_t>(warps) * p.stages * kStageBytes;
   StreamShared& S = *reinterpret_cast<StreamShared*>(xs + static_cast<size_t>(cols) * p.xstride);
-  float* xscale = reinterpret_cast<float*>(&S + 1);  // DIGITS: 2^e of each chunk
+  float* xscale = reinterpret_cast<float*>(&S + 1);  // DIGITS: of each chunk, of the highest digit; 0: 16 bits
   float* part = xscale + (DIGITS ? p.chunks : 0);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
@@ -434,6 +474,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   const uint32_t x_lane = smem_addr(xs) + static_cast<uint32_t>(min(g, cols - 1)) * p.xstride;
   const uint32_t w_lane = smem_addr(my_ring) + static_cast<uint32_t>(gr) * 128;
   constexpr uint32_t kXChunk = kChunkK * (DIGITS ? 1 : 2);
+  // DIGITS: what a digit in this lane's two columns counts, next to the highest; columns past it, 0
+  const float weight0 = t <= (kDigits - 1) / 2 ? power_of_2(8 * (2 * t - (kDigits - 1))) : 0.0f;
+  const float weight1 = t < (kDigits - 1) / 2 ? power_of_2(8 * (2 * t + 1 - (kDigits - 1))) : 0.0f;
   bool ok = true;
   int stage = 0, done = 0;  // pairs before `done` are stored
   uint32_t phase = 0;
@@ -449,33 +492,45 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         if constexpr (DIGITS) {
           const uint4 v = xv;
           // magnitudes of a 16-bit type compare as whole numbers
-          const uint32_t two = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                        __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-          const uint32_t most = __float_as_uint(
-              unpack2<T>(__reduce_max_sync(~0u, max(two & 0xFFFFu, two >> 16))).x);
-          const int e = -digit_exponent(most);
-          const float f1 = __int_as_float((127 + e / 2) << 23);
-          const float f2 = __int_as_float((127 + e - e / 2) << 23);
-          const float2 p01 = unpack2<T>(v.x), p23 = unpack2<T>(v.y), p45 = unpack2<T>(v.z),
-                       p67 = unpack2<T>(v.w);
-          // bytes of a word's low nibbles: columns 0, 4, 1, 5; of its high ones: 2, 6, 3, 7
-          const float low[4] = {p01.x, p45.x, p01.y, p45.y};
-          const float high[4] = {p23.x, p67.x, p23.y, p67.y};
-          uint32_t dl[3], dh[3];
-          digits4(low, f1, f2, dl);
-          digits4(high, f1, f2, dh);
-          // one word: its low nibbles' digits, then its high ones'; two words: both low, then both high
-          const int i = c * 32 + lane, at = SUB == 1 ? 2 * i : (i & ~1) * 2 + (i & 1);
+          const uint32_t m[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+          const uint32_t two = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+          const uint32_t most = __reduce_max_sync(~0u, max(two & 0xFFFFu, two >> 16));
+          uint32_t least = 0;
+          if (std::is_same<T, __nv_bfloat16>::value) {
+            uint32_t l[4];  // 0x8000 less the magnitude, and 0 for 0
 #pragma unroll
-          for (int d = 0; d < 3; ++d) {
-            uint32_t* out = reinterpret_cast<uint32_t*>(xs + static_cast<size_t>(d) * p.xstride);
-            out[at] = dl[d];
-            out[at + (SUB == 1 ? 1 : 2)] = dh[d];
+            for (int i = 0; i < 4; ++i) l[i] = (0x80008000u - m[i]) & 0x7FFF7FFFu;
+            const uint32_t both = __vmaxu2(__vmaxu2(l[0], l[1]), __vmaxu2(l[2], l[3]));
+            least = __reduce_max_sync(~0u, max(both & 0xFFFFu, both >> 16));
+          }
+          constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+          bool exact;
+          const int e = digit_exponent<T>(most, least, exact);
+          exact = exact && most < kInf;
+          uint8_t* out = xs + c * kChunkK;
+          if (exact) {
+            const float2 p01 = unpack2<T>(v.x), p23 = unpack2<T>(v.y), p45 = unpack2<T>(v.z),
+                         p67 = unpack2<T>(v.w);
+            // bytes of a word's low nibbles: columns 0, 4, 1, 5; of its high ones: 2, 6, 3, 7
+            const uint64_t low[2] = {f32x2_pack(p01.x, p45.x), f32x2_pack(p01.y, p45.y)};
+            const uint64_t high[2] = {f32x2_pack(p23.x, p67.x), f32x2_pack(p23.y, p67.y)};
+            uint32_t dl[kDigits], dh[kDigits];
+            digits4(low, e, dl);
+            digits4(high, e, dh);
+            // one word: its low nibbles' digits, then its high ones'; two words: both low, then both high
+            const int at = SUB == 1 ? 2 * lane : (lane & ~1) * 2 + (lane & 1);
+#pragma unroll
+            for (int d = 0; d < kDigits; ++d) {
+              uint32_t* words = reinterpret_cast<uint32_t*>(out + static_cast<size_t>(d) * p.xstride);
+              words[at] = dl[d];
+              words[at + (SUB == 1 ? 1 : 2)] = dh[d];
+            }
+          } else {  // 512 bytes in the places of the first two digits
+            *reinterpret_cast<uint4*>(out + lane / 16 * p.xstride + lane % 16 * 16) = v;
           }
           // 16 lo + hi is 16 times the sum
           if (lane == 0)
-            xscale[c] = most >= 0x7F800000u ? __int_as_float(0x7FC00000)
-                                            : ldexpf(SUB > 1 ? 0.0625f : 1.0f, -e);
+            xscale[c] = exact ? power_of_2(e + 8 * (kDigits - 1) - (SUB > 1 ? 4 : 0)) : 0.0f;
           if (nq == 0) load_x(nc);
         } else {
           if (ok) ok = __all_sync(~0u, mbar_wait_bounded(&S.x_full, 0, abort));
@@ -497,17 +552,30 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         const bool two = u0 + 2 * pair + 1 < u1;
         if constexpr (DIGITS) {
           float chunk[2][4] = {};
-          if (two) add_chunk_digits<T, SUB, ZP, true>(chunk, cur, w, 16u * gr, x, t, gr);
-          else add_chunk_digits<T, SUB, ZP, false>(chunk, cur, w, 16u * gr, x, t, gr);
           const float f = xscale[c];
+          float w0 = weight0, w1 = weight1;
+          if (f != 0.0f) {
+            if (two) add_chunk_digits<T, SUB, ZP, true>(chunk, cur, w, 16u * gr, x, t, gr);
+            else add_chunk_digits<T, SUB, ZP, false>(chunk, cur, w, 16u * gr, x, t, gr);
+            w0 *= f;
+            w1 *= f;
+          } else {  // every column is the token: the highest digit's place takes it
+            const uint32_t x16 = smem_addr(xs) + kXChunk * c, gap = p.xstride - 256;
+            if (two) add_chunk_16<T, SUB, ZP, true>(chunk, cur, w, 16u * gr, x16, gap, t, gr);
+            else add_chunk_16<T, SUB, ZP, false>(chunk, cur, w, 16u * gr, x16, gap, t, gr);
+            w0 = t == (kDigits - 1) / 2 ? 1.0f : 0.0f;
+            w1 = 0.0f;
+          }
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) acc[r][d] = fmaf(f, chunk[r][d], acc[r][d]);
+          for (int r = 0; r < 4; ++r) {
+            float* a = &acc[r / 2][2 * (r & 1)];
+            const float* v = &chunk[r / 2][2 * (r & 1)];
+            a[0] = fmaf(w0, v[0], a[0]);
+            a[1] = fmaf(w1, v[1], a[1]);
           }
         } else {
-          if (two) add_chunk_16<T, SUB, ZP, true>(acc, cur, w, 16u * gr, x, t, gr);
-          else add_chunk_16<T, SUB, ZP, false>(acc, cur, w, 16u * gr, x, t, gr);
+          if (two) add_chunk_16<T, SUB, ZP, true>(acc, cur, w, 16u * gr, x, 0, t, gr);
+          else add_chunk_16<T, SUB, ZP, false>(acc, cur, w, 16u * gr, x, 0, t, gr);
         }
       }
       __syncwarp();
@@ -516,14 +584,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       q = nq;
       c = nc;
     }
-    // the pair's partial sums, [column][row] of each warp, in the last 2 batch pairs' places
+    // the pair's partial sums, [token][row] of each warp, in the last 2 batch pairs' places
     float* mine = part + (pair % (2 * p.batch) * warps + warp) * part_floats;
+    if constexpr (DIGITS) {  // the columns, all of one token, are added up over the quad
+      float v[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = 2 * t + h;
-      if (m < cols) {
+      for (int r = 0; r < 4; ++r) {
+        v[r] = acc[r / 2][2 * (r & 1)] + acc[r / 2][2 * (r & 1) + 1];
+        v[r] += __shfl_xor_sync(~0u, v[r], 1);
+        v[r] += __shfl_xor_sync(~0u, v[r], 2);
+      }
+      mine[gr + 8 * t] = t == 0 ? v[0] : t == 1 ? v[1] : t == 2 ? v[2] : v[3];
+    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mine[m * 32 + gr + 8 * r] = acc[r / 2][2 * (r & 1) + h];
+      for (int h = 0; h < 2; ++h) {
+        const int m = 2 * t + h;
+        if (m < cols) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) mine[m * 32 + gr + 8 * r] = acc[r / 2][2 * (r & 1) + h];
+        }
       }
     }
     if ((pair + 1) % p.batch != 0 && pair + 1 < pairs) continue;
@@ -532,20 +611,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     for (int o = (warp + pair) % warps; o < (pair + 1 - done) * p.M; o += warps) {
       const int from = done + o / p.M, m = o % p.M;
       const float* sums = part + from % (2 * p.batch) * warps * part_floats + lane;
-      float v;
-      if constexpr (DIGITS) {
-        float d[3] = {};
+      float v = 0.0f;
 #pragma unroll 8
-        for (int w = 0; w < warps; ++w) {
-#pragma unroll
-          for (int e = 0; e < 3; ++e) d[e] += sums[w * part_floats + e * 32];
-        }
-        v = fmaf(d[2], 65536.0f, fmaf(d[1], 256.0f, d[0]));
-      } else {
-        v = 0.0f;
-#pragma unroll 8
-        for (int w = 0; w < warps; ++w) v += sums[w * part_floats + m * 32];
-      }
+      for (int w = 0; w < warps; ++w) v += sums[w * part_floats + m * 32];
       const int n = (u0 + 2 * from) * kUnitRows + lane;
       if (n < min(p.N, u1 * kUnitRows)) {
         if (p.bias) v += to_f32(static_cast<const T*>(p.bias)[n]);
@@ -569,6 +637,7 @@ namespace {
 
 struct StreamPlan {
   int warps, per_sm, stages, xstride, batch;
+  bool digits;
   size_t smem;
 };
 
@@ -586,22 +655,20 @@ struct Shape { int warps, per_sm; };
 constexpr Shape kFewChunks[] = {{8, 2}, {8, 1}, {16, 1}}, kManyChunks[] = {{16, 1}, {8, 1}};
 constexpr int kMany = 32;
 
-bool plan_stream(int M, int K, int group, StreamPlan& s) {
-  if (M > kMaxTok) return false;
-  const bool digits = M == 1;
-  const int sub = sub_of(group), cols = digits ? 3 : M;
+bool plan_shapes(int M, int K, int group, bool digits, const Shape* shapes, int n, StreamPlan& s) {
+  const int sub = sub_of(group), cols = digits ? kDigits : M;
   const int chunks = (K + kChunkK - 1) / kChunkK;
+  s.digits = digits;
   // a column's activations up to the last chunk's end, and a pad that sets the quads of two columns
   // apart: 8, 16 or 32 bytes a lane of digits, twice that in 16 bits
   s.xstride = chunks * kChunkK * (digits ? 1 : 2) +
               (digits ? (sub == 1 ? 32 : sub == 2 ? 64 : 16) : (sub == 1 ? 64 : 16));
-  const Shape* shapes = chunks < kMany ? kFewChunks : kManyChunks;
-  for (int i = 0; i < (chunks < kMany ? 3 : 2); ++i) {
+  for (int i = 0; i < n; ++i) {
     const Shape& shape = shapes[i];
     s.warps = shape.warps;
     s.per_sm = shape.per_sm;
     const size_t most = shape.per_sm == 2 ? kSmemMost / 2 : kSmemMost;
-    const size_t pair_bytes = static_cast<size_t>(s.warps) * 32 * cols * sizeof(float);
+    const size_t pair_bytes = static_cast<size_t>(s.warps) * 32 * M * sizeof(float);
     const size_t fixed = 1024 + static_cast<size_t>(cols) * s.xstride + sizeof(StreamShared) +
                          (digits ? chunks * sizeof(float) : 0);
     for (s.stages = kMaxStages; s.stages >= 2; --s.stages) {
@@ -613,6 +680,16 @@ bool plan_stream(int M, int K, int group, StreamPlan& s) {
     }
   }
   return false;
+}
+
+bool plan_stream(int M, int K, int group, StreamPlan& s) {
+  if (M > kMaxTok) return false;
+  const bool many = K > (kMany - 1) * kChunkK;
+  const Shape* shapes = many ? kManyChunks : kFewChunks;
+  // one token: digits where the first of the shapes holds them, 5 bytes a column, and 16 bits beyond (K
+  // = 18432, N = 16384: 33 us in digits; K = 24576: 45 us in 16 bits)
+  return (M == 1 && plan_shapes(M, K, group, true, shapes, 1, s)) ||
+         plan_shapes(M, K, group, false, shapes, many ? 2 : 3, s);
 }
 
 template <typename T, int SUB, bool ZP, bool DIGITS>
@@ -648,7 +725,7 @@ cudaError_t launch_sub(const CUtensorMap (&map)[2], const StreamArgs& p, const S
 template <typename T>
 cudaError_t launch_typed(const CUtensorMap (&map)[2], const StreamArgs& p, const StreamPlan& s,
                          int grid, cudaStream_t stream) {
-  if (p.M == 1)
+  if (s.digits)
     return p.zeros ? launch_sub<T, true, true>(map, p, s, grid, stream)
                    : launch_sub<T, false, true>(map, p, s, grid, stream);
   return p.zeros ? launch_sub<T, true, false>(map, p, s, grid, stream)
