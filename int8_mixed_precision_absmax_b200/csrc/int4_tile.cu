@@ -110,7 +110,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // The scales and zero points of NG consecutive groups of a row, from group g (a multiple of NG) on.
-// Groups past the row's end repeat the last one (they meet zero activations only).
+// Groups past the row's end repeat the last one (their weights are not used).
 template <int NG>
 struct RowGroups {
   uint32_t s[(NG + 1) / 2], z;  // two scales, four zero points to a word
@@ -333,6 +333,15 @@ __global__ void __launch_bounds__(threads_of(TW), TW == 4 ? 2 : 1)
           tmem_st16(to + 16 * c, out);
         }
         if (!ok) break;
+        // Past the row's end, where the codes' place is filled with zeros, (0 - z) times the scale may be
+        // an infinity, and X's 0 times that a NaN: zeros in its place.  (16 tokens of 12288 x 49152, us:
+        // 109 without, 110 so, 115 with a test of each chunk, 120 where the MMAs stopped at the row's end.)
+        const int chunks = p.K / 32 - k * (kStepK / 32) - first;
+        if (chunks < kChunks) {
+          const uint32_t none[16] = {};
+          tmem_st_wait();
+          for (int c = max(chunks, 0); c < kChunks; ++c) tmem_st16(to + 16 * c, none);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
