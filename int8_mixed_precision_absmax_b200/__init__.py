@@ -700,10 +700,24 @@ class _BlockEnds:
     post_norm: BlockNorm | None = None
     _dtype = torch.float16  # of the product's activations
 
-    def _before(self, X: torch.Tensor) -> torch.Tensor:
-        X2 = X.reshape(-1, X.shape[-1]).contiguous()
-        if self.pre_norm is None:
-            return X2
+    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None,
+                 residual: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                 x_scale: float = 1.0, f_scale: float = 1.0) -> torch.Tensor:
+        if residual is None and (gate is not None or self.post_norm is not None
+                                 or x_scale != 1.0 or f_scale != 1.0):
+            raise ValueError("gate, x_scale, f_scale and post_norm act where the layer's output "
+                             "is added to a residual")
+        rows = X.dim() == 2  # then neither X nor the result needs another shape
+        X2 = (X if rows else X.reshape(-1, X.shape[-1])).contiguous()
+        if self.pre_norm is not None:
+            X2 = self._before(X2)
+        if residual is None:
+            Y = self._product(X2, out)
+        else:
+            Y = self._after(self._product(X2, None), residual, gate, x_scale, f_scale, out)
+        return Y if rows else Y.reshape(*X.shape[:-1], self.out_features)
+
+    def _before(self, X2: torch.Tensor) -> torch.Tensor:
         h = None
         if X2.dtype is torch.float32 and self.pre_norm.weight is None:
             h = X2.new_empty(X2.shape, dtype=self._dtype)  # nothing else says the layer's type
@@ -717,16 +731,6 @@ class _BlockEnds:
             post_bias=post and post.bias, gate=gate, x_scale=x_scale, f_scale=f_scale,
             eps=post.eps if post is not None else 1e-6,
             layer_norm=post is not None and post.layer_norm, y=out)[0]
-
-    def _finish(self, product, X, residual, gate, x_scale, f_scale, out):
-        """product(X2, out) between the block's ends."""
-        if residual is None and (gate is not None or self.post_norm is not None
-                                 or x_scale != 1.0 or f_scale != 1.0):
-            raise ValueError("gate, x_scale, f_scale and post_norm act where the layer's output "
-                             "is added to a residual")
-        if residual is None:
-            return product(self._before(X), out)
-        return self._after(product(self._before(X), None), residual, gate, x_scale, f_scale, out)
 
 
 class Int8Linear(_BlockEnds):
@@ -769,15 +773,7 @@ class Int8Linear(_BlockEnds):
             self._ws_rows = M
         return self._workspace
 
-    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None,
-                 residual: torch.Tensor | None = None, gate: torch.Tensor | None = None,
-                 x_scale: float = 1.0, f_scale: float = 1.0) -> torch.Tensor:
-        lead = X.shape[:-1]
-        Y = self._finish(self._product, X, residual, gate, x_scale, f_scale, out)
-        return Y.reshape(*lead, self.out_features)
-
     def _product(self, X2: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
-        X2 = X2.reshape(-1, self.in_features)
         ws = self._ws(X2.shape[0], X2.device)
         if self.per_tensor_activation:
             return int8_linear_forward_ex(X2, self.Wq, self.w_scale, self.bias, self.threshold,
@@ -815,13 +811,6 @@ class Int4Linear(_BlockEnds):
     def dequantize(self) -> torch.Tensor:
         """The weight the codes stand for, [out, in]."""
         return int4_dequant_weight(self.codes, self.scales, self.zeros, self.group_size)
-
-    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None,
-                 residual: torch.Tensor | None = None, gate: torch.Tensor | None = None,
-                 x_scale: float = 1.0, f_scale: float = 1.0) -> torch.Tensor:
-        lead = X.shape[:-1]
-        Y = self._finish(self._product, X, residual, gate, x_scale, f_scale, out)
-        return Y.reshape(*lead, self.out_features)
 
     def _product(self, X2: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
         return int4_linear_forward(X2, self.codes, self.scales, self.zeros, self.bias,
