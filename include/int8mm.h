@@ -333,8 +333,8 @@ int int8_linear_forward_noalloc(const void *X, int M, int K, const int8_t *Wq,
  *   zeros   uint8 [N, ceil(K/group)] whole numbers 0..15, or NULL: every zero point is 8
  * and they stand for W_hat[n,k] = scales[n,c] * (u[n,k] - zeros[n,c]), c = k / group.
  * group is 32, 64 or a multiple of 128 (else INT8MM_ERR_GROUP); it may exceed K, and the last
- * group of a row may be short.  K must be a multiple of 32, 1 <= K <= INT8MM_MAX_K, 1 <= M, N <= INT8MM_MAX_ROWS.  The
- * conventions at the top of this file hold for these calls too.
+ * group of a row may be short.  K must be a multiple of 32, 1 <= K <= INT8MM_MAX_K, and
+ * 1 <= M, N <= INT8MM_MAX_ROWS.  The conventions at the top of this file hold for these calls too.
  */
 
 /*
@@ -392,7 +392,8 @@ int int4_linear_forward(const void *X, int M, int K, const uint8_t *codes, const
  *   n(v) = v / sqrt(mean(v^2) + eps), or, with INT8MM_LAYER_NORM,
  *   n(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps),
  * w NULL = all ones, b NULL = all zeros; statistics and products in float32, rounded once where
- * a result is stored.  eps >= 0 and finite (else INT8MM_ERR_VALUE).
+ * a result is stored: rows (bfloat16 or float32) whose squares do not add up below 2^128 are beyond
+ * them and come out as zeros or NaN.  eps >= 0 and finite (else INT8MM_ERR_VALUE).
  */
 
 /*

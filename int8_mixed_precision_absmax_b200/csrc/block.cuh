@@ -96,7 +96,8 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t o
 }
 
 // W_hat of 4-bit words: the group's constants, and 8 values of a word.  A nibble set into the low
-// mantissa bits of 1024 (fp16) or 128 (bf16) reads as that number plus the code.  LOP3: masks and
+// mantissa bits of 1024 (fp16) or 128 (bf16) reads as that number plus the code (Kim, Henry, Fahim and
+// Awadalla, "Who Says Elephants Can't Run", 2022, for fp16).  LOP3: masks and
 // sets a nibble by the one instruction; the tensor-core kernel, bound by its instructions, gains
 // by it (107 us against 119 for 16 tokens of 12288 x 49152), the inverse quantizer, bound by
 // memory, does better with what the compiler chooses (273 us against 299 for the same weights).

@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Other groups (multiples of 128, or a whole row): one warp per group, which it reads twice.
+// Other groups (multiples of 128, or a whole row): one warp per group, which it reads twice, with nothing
+// asked for ahead: 49152 x 12288, groups of 512 492 us, of 1024 310, one for each row 459 (231 of bytes).
 template <typename T, bool AFFINE>
 __global__ void __launch_bounds__(kThreads)
     int4_quant_long_kernel(const T* __restrict__ W, int N, int K, int group, int groups,

@@ -27,8 +27,9 @@
 // 128) by one logic instruction, less that number and the zero point, for two weights at a time.  (MMAs
 // on the codes alone, the zero point by a sum of the activations, saved the subtractions but took
 // half as many MMAs again: 8 tokens of 4096 x 4096 6.9 us, against 6.2; 3 tokens of 13824 x 5120 18.3,
-// 17.1.  One token of 12288 x 49152 takes 74 us this way, 53 with digits; two tokens 74 with digits, 65
-// this way.)
+// 17.1.  One token, us in digits / this way: N = 49152, K = 12288 53 / 74, N = 32768, K = 4096 15.9 /
+// 20.9, N = 4096, K = 8192 8.0 / 8.5, K = 4096 5.9 / 5.7.  The digits of two tokens are more columns than
+// an MMA has.)
 //
 // Either way the group's scale meets the float32 sum of the group: the weights are never rounded.
 // Which k a lane takes is free as long as both operands agree: lane t of a quad takes neighbouring
@@ -647,10 +648,10 @@ int sub_of(int group) { return group == 32 ? 1 : group == 64 ? 2 : 4; }
 // The block's shape, the first of an order that fits, at least two stages for each warp.  One block of
 // 16 warps brings the activations into shared memory once an SM and lets all warps share the chunks,
 // but with few of them a warp has one in a pair, and waits; two blocks of 8 also fill each other's
-// pauses.  (us of two blocks of 8 / one of 16 / one of 8; K = 4096: one token, N 4096 6.3 / 6.7 / 6.1,
-// N 32768 16.4 / 25.4 / 20.6, 3 tokens 5.9 / 6.6 / 6.0, 19.3 / 22.0 / 24.1, 6 tokens, N 4096 - / 7.0 /
-// 6.5; K = 8192: one token, N 4096 9.3 / 8.4 / 8.7, 3 tokens, N 32768 - / 35.4 / 40.0; K = 12288: one
-// token, N 49152 56.3 / 53.5 / 70.0, 3 tokens, N 32768 - / 48.3 / 55.5.)
+// pauses.  (us of two blocks of 8 / one of 16 / one of 8; K = 4096: one token, N 4096 6.0 / 6.0 / 5.6,
+// N 32768 15.9 / 20.9 / 19.5, 3 tokens 5.9 / 6.3 / 5.7, 18.6 / 20.9 / 22.9, 6 tokens, N 4096 - / 6.5 /
+// 5.8; K = 8192: one token, N 4096 - / 8.0 / 8.6, 3 tokens, N 32768 - / 35.5 / 40.0; K = 12288: one
+// token, N 49152 - / 53.3 / 68.3, 3 tokens, N 32768 - / 48.5 / 55.9.)
 struct Shape { int warps, per_sm; };
 constexpr Shape kFewChunks[] = {{8, 2}, {8, 1}, {16, 1}}, kManyChunks[] = {{16, 1}, {8, 1}};
 constexpr int kMany = 32;
@@ -736,9 +737,9 @@ cudaError_t launch_typed(const CUtensorMap (&map)[2], const StreamArgs& p, const
 
 // Where the activations leave room for one block of 8 warps only, though they are of few columns (8
 // tokens), instructions bound the kernel, and many units to a block are better off with the tensor
-// cores.  (us of this / of int4_tile.cu, N = 11008, 32768; 8 tokens, K = 2048 8.6 / 9.6, 17.6 / 15.2,
-// K = 4096 12.7 / 12.8, 27.7 / 26.0, K = 8192 21.1 / 21.6, 44.9 / 46.5; 6 tokens, K = 4096 12.0 / 12.8,
-// 25.7 / 25.9; 4 tokens, K = 12288 27.2 / 29.8, 59.5 / 66.8.)
+// cores.  (us of this / of int4_tile.cu, N = 11008, 32768; 8 tokens, K = 2048 8.2 / 9.2, 16.7 / 14.2,
+// K = 4096 12.3 / 12.4, 25.9 / 23.8, K = 8192 19.0 / 19.0, 43.0 / 43.1; 6 tokens, K = 4096 11.5 / 12.4,
+// 24.0 / 23.8; 4 tokens, K = 12288 24.4 / 25.1, 56.0 / 63.1.)
 bool int4_stream_suits(int M, int N, int K, int group, int num_sms) {
   StreamPlan s;
   if (!plan_stream(M, K, group, s)) return false;

@@ -19,12 +19,16 @@
 //
 // Measured, us: 2048 tokens of 4096 x 11008, groups of 128, 144 (1280 TFLOP/s, 77 % of the measured
 // bf16 rate of the tensor cores alone; 165 in a long run under the power cap); 77 tokens of the same
-// 15.7 (1.8 TB/s), 16 tokens of 12288 x 49152 107 (2.9 TB/s).  With many tokens the MMAs bound it, which
-// read A from tensor memory while the dequantizing warps write it; with few the instructions of the
-// dequantizing, 13 for 8 weights and the steps around them, and the start and joining of a cluster.
+// 15.0 (1.8 TB/s), 16 tokens 12.5, and of 12288 x 49152 107 (2.9 TB/s).  With many tokens the MMAs bound
+// it, which read A from tensor memory while the dequantizing warps write it.  With few no pipe does: 16
+// tokens of 12288 x 8192 issue an instruction in 54 % of a scheduler's active cycles, none of its pipes
+// is above 40 %, and of 1830 instructions a step the dequantizing arithmetic (13 for 8 weights) is 832;
+// what is left are the waits between the roles, once a step, with two or three steps of W_hat in tensor
+// memory to cover them, and the start and joining of a cluster.
 //
-// Every wait is bounded (ptx.cuh); a wait that gives up reports INT8MM_ERR_TIMEOUT, and the block
-// drains its copies and MMAs, frees its tensor memory and exits.
+// Every wait on a barrier is bounded (ptx.cuh); a wait that gives up reports INT8MM_ERR_TIMEOUT, and the
+// block drains its copies and MMAs, frees its tensor memory and exits.  The allocation of tensor memory
+// waits without a bound; plan_tile sizes shared memory so that it need not wait for a kernel here.
 #include <type_traits>
 
 #include "block.cuh"
