@@ -77,6 +77,19 @@ __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, vola
   return mbar_wait_bounded(bar, parity, abort);
 }
 
+// ---------------------------------------------------------------- ahead of a wait
+
+// The box of a 2-D tiled load, brought as far as L2: no value of it reaches the SM.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // ---------------------------------------------------------------- 4-bit weights
 //
 // Of the 8 neighbours k = 8j .. 8j+7 in a 32-bit word, nibble i (from the low end) holds
