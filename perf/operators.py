@@ -261,8 +261,9 @@ def run(state):
         return i8.int8_block_norm(s["x"], s["weight"], s["bias"], EPS, c["layer_norm"], h=s["h"])
     y, h = i8.int8_block_residual(s["f"], s["x"], post_norm=c["post"], post_weight=s["post_weight"],
                                   post_bias=s["post_bias"], gate=s["gate"], x_scale=s["x_scale"],
-                                  f_scale=s["f_scale"], next_norm=c["next"], next_weight=s["weight"],
-                                  next_bias=s["bias"], eps=EPS, layer_norm=c["layer_norm"], y=s["y"],
+                                  f_scale=s["f_scale"], next_norm=c["next"],
+                                  next_weight=s["weight"] if c["next"] else None,
+                                  next_bias=s["bias"] if c["next"] else None, eps=EPS, layer_norm=c["layer_norm"], y=s["y"],
                                   h=s["h"] if c["next"] else None)
     return dict(y=y, h=h) if c["next"] else dict(y=y)
 
